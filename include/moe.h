@@ -326,6 +326,103 @@ int moe_expert_ffn_noalloc(const void *x_bf16, const int32_t *expert_offsets,
  * nothing.  The paper has no counterpart. */
 int moe_noalloc_read_status(int *status_out, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Low-rank adapters of many requests beside one shared projection.  The
+ * pages have no counterpart: the calls serve and tune adapters on a layer
+ * whose own weights stay frozen -- its router (logits for moe_route, from
+ * its x_bf16 == NULL form), any other projection of the token rows, or the
+ * layer's output.
+ *
+ *  adapter [T] int32: the adapter of each row, in [0, n), or MOE_EMPTY_SLOT
+ *    for a row without one; rows come in any order.  Another value sets
+ *    MOE_ERR_DEVICE_CHECK in the workspace's status word and counts as none.
+ *  lora_a [n x r x din], lora_b [n x r x dout] bf16, BOTH by rank (row j of
+ *    an adapter's matrix belongs to rank j; moe_pack_w_down with E = n,
+ *    d = dout, I = r makes lora_b from [n x dout x r]).  Adapters of a lower
+ *    rank are padded with zero rows.
+ *  scale [n] float32 or NULL (1): the factor s_a of each adapter.
+ *  Shapes: 0 <= T <= 2^20, din and dout multiples of 8 in [8, 16384],
+ *    1 <= r <= 128, 1 <= n <= 1024.  Every tensor is 16-byte aligned
+ *    (adapter, scale and bias: 4-byte).  Outputs overlap no input and no
+ *    other output.
+ *  Workspace: at least moe_adapter_workspace_size(...) bytes for these
+ *    shapes, initialised with moe_workspace_init; one serves both calls.
+ *    The calls are deterministic.
+ *
+ * moe_adapter_linear: u[t] = s_a A_a x_t,  y[t] = W x_t + bias + B_a^T u[t].
+ *   w_bf16 [dout x din]; y [T x dout] of y_dtype (MOE_DTYPE_*), rounded once.
+ *   w_bf16 NULL: y is read and the adapters' part (and bias) added to it --
+ *   beside a product that another call made, moe_layer's y for one.
+ *   bias [dout] float32 or NULL.  u_out [T x r] float32 (nullable) receives
+ *   u, 0 in rows without an adapter, for the backward call.
+ * moe_adapter_backward: with v[t] = s_a B_a dy_t,
+ *     dx[t] = W^T dy_t + A_a^T v[t]         [T x din] of dx_dtype
+ *     d_lora_a[a] = sum_{t of a} v[t] x_t^T [n x r x din] float32
+ *     d_lora_b[a] = sum_{t of a} u[t] dy_t^T [n x r x dout] float32
+ *   dy_bf16 [T x dout]; u from the forward call; w_t_bf16 [din x dout] the
+ *   transposed weights (laid out once, they are frozen), needed with dx.
+ *   dx NULL: not computed.  w_t_bf16 NULL with dx: dx is read and A_a^T v[t]
+ *   added to it.  d_lora_a and d_lora_b are each nullable and are
+ *   overwritten; adapters without rows get zeros (T = 0: all of them). */
+size_t moe_adapter_workspace_size(int T, int din, int dout, int r, int n);
+int moe_adapter_linear(const void *x_bf16, const void *w_bf16, const float *bias,
+                       const int32_t *adapter, const void *lora_a_bf16, const void *lora_b_bf16,
+                       const float *scale, int T, int din, int dout, int r, int n, void *y,
+                       int y_dtype, float *u_out, void *ws, size_t ws_bytes, void *stream);
+int moe_adapter_backward(const void *dy_bf16, const void *x_bf16, const void *w_t_bf16,
+                         const int32_t *adapter, const void *lora_a_bf16, const void *lora_b_bf16,
+                         const float *scale, const float *u, int T, int din, int dout, int r,
+                         int n, void *dx, int dx_dtype, float *d_lora_a, float *d_lora_b, void *ws,
+                         size_t ws_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Training a router: the losses that keep its experts evenly used, with the
+ * per-expert counts, and the gradient of its logits.  The pages' method is
+ * inference only; Eq. 2 ("Paper of the Week #3", section "The Receipt") is
+ * differentiated here as it is routed there.
+ *
+ *  logits [T x E] float32, topk_idx [T x k1] as moe_route, moe_route_cascade
+ *    and moe_route_skip write them (MOE_EMPTY_SLOT slots hold no expert; an
+ *    id outside [0, E) sets MOE_ERR_DEVICE_CHECK in the workspace's status
+ *    word and is passed over; an id that repeats in a row counts each time).
+ *  token_mask [T] bytes or NULL: rows of a zero byte are padding -- nothing
+ *    in them is read, they count nowhere and their gradient is 0.  A row
+ *    whose logits are all -inf has no distribution and is treated the same.
+ *    Single -inf logits are experts of probability 0.
+ *  Shapes: 0 <= T <= 2^20, 1 <= E <= 1024, 1 <= k1 <= min(E, 32).  logits,
+ *    topk_idx, dlogits and the workspace are aligned as everywhere; masks
+ *    need no alignment, scalars and counts 4 bytes.  Outputs overlap no
+ *    input.  The calls are deterministic.
+ *
+ * moe_balance_loss: N counting tokens, n_e their slots on expert e, R the sum
+ *   of n_e, p_t = softmax(z_t), lse_t = log sum_e exp(z_te):
+ *     P_e = (1/N) sum_t p_te,  L_bal = E sum_e (n_e / R) P_e,
+ *     L_z = (1/N) sum_t lse_t^2
+ *   counts [E + 1] int32: n_e, and N behind them; loss [3] float32:
+ *   balance_coef L_bal + z_coef L_z, L_bal, L_z; prob_mean [E] float32
+ *   (nullable): P_e.  N = 0 gives zeros.  NaN or +inf logits in a counting
+ *   row make losses and P_e NaN.  ws: moe_balance_workspace_size bytes,
+ *   initialised with moe_workspace_init.
+ * moe_route_backward: dlogits [T x E] of dz_dtype (MOE_DTYPE_*, rounded
+ *   once), the sum of two parts, each left out when its input is NULL:
+ *   - d_topk_w [T x k1] float32, the gradient of the Eq. 2 weights: with K2
+ *     the row's given experts and, of the others, those of the largest
+ *     logits (equal ones by the lower index), min(k2, E) in all, and w the
+ *     softmax over K2, dz_m = w_m (g_m - sum_i g_i w_i) in K2, 0 elsewhere.
+ *     Entries of empty slots are not used.
+ *   - counts [E + 1] from moe_balance_loss (or summed over several batches
+ *     or ranks): the gradient of balance_coef L_bal + z_coef L_z, the counts
+ *     held fixed, times d_loss (device float32 scalar, NULL: 1).
+ *   k1 <= k2; k2 >= E: all experts.  ws (nullable) takes the status word. */
+size_t moe_balance_workspace_size(int T, int E);
+int moe_balance_loss(const float *logits, const int32_t *topk_idx, const unsigned char *token_mask,
+                     int T, int E, int k1, float balance_coef, float z_coef, int32_t *counts,
+                     float *loss, float *prob_mean, void *ws, size_t ws_bytes, void *stream);
+int moe_route_backward(const float *logits, const int32_t *topk_idx, const float *d_topk_w,
+                       const int32_t *counts, const unsigned char *token_mask, int T, int E,
+                       int k1, int k2, float balance_coef, float z_coef, const float *d_loss,
+                       void *dlogits, int dz_dtype, void *ws, size_t ws_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

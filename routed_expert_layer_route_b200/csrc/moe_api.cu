@@ -11,6 +11,8 @@
 
 #include "../../include/moe.h"
 #include "../../include/moe_testing.h"
+#include "adapter.cuh"
+#include "balance.cuh"
 #include "combine.cuh"
 #include "ctopk.cuh"
 #include "decode.cuh"
@@ -1499,3 +1501,303 @@ extern "C" int moe_noalloc_read_status(int *status_out, void *stream)
     *status_out = v;
     return MOE_OK;
 }
+
+// ========================================================================== adapters
+namespace moe {
+
+constexpr int kAdMaxDim = 16384, kAdMaxR = 128, kAdMaxN = 1024;
+
+struct AdLayout {
+    size_t inner, total;
+};
+
+static AdLayout ad_layout(int T, int din, int dout, int r, int n)
+{
+    (void)din;
+    (void)dout;
+    (void)n;
+    AdLayout L;
+    size_t o = sizeof(WsHeader);
+    L.inner = o;   o = align256(o + sizeof(float) * (size_t)T * r);
+    L.total = o;
+    return L;
+}
+
+static int ad_check(int T, int din, int dout, int r, int n)
+{
+    if (T < 0 || T > kMaxT || r < 1 || r > kAdMaxR || n < 1 || n > kAdMaxN)
+        return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (din < 8 || din > kAdMaxDim || din % 8 || dout < 8 || dout > kAdMaxDim || dout % 8)
+        return MOE_ERR_UNSUPPORTED_SHAPE;
+    return MOE_OK;
+}
+
+static bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
+
+static int ad_check_ws(const void *ws, size_t ws_bytes, size_t need)
+{
+    if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255))
+        return MOE_ERR_INVALID_ARG;
+    return ws_bytes < need ? MOE_ERR_WORKSPACE_TOO_SMALL : MOE_OK;
+}
+
+static int enqueue_ad_inner(AdInnerArgs a, cudaStream_t s)
+{
+    const int64_t items = (int64_t)a.T * a.r;
+    return launch(k_ad_inner, dim3((unsigned)((items + 7) / 8)), dim3(256), 0, s, kPdl, a);
+}
+
+static int enqueue_ad_product(AdProductArgs a, cudaStream_t s)
+{
+    return launch(k_ad_product, dim3((a.dout + 63) / 64, (a.T + 63) / 64), dim3(256), 0, s, kPdl, a);
+}
+
+static int enqueue_ad_outer(AdOuterArgs a, cudaStream_t s)
+{
+    return launch(k_ad_outer, dim3((a.D + 127) / 128, a.r, a.n), dim3(128), 0, s, kPdl, a);
+}
+
+}  // namespace moe
+
+extern "C" {
+
+size_t moe_adapter_workspace_size(int T, int din, int dout, int r, int n)
+{
+    return ad_check(T, din, dout, r, n) == MOE_OK ? ad_layout(T, din, dout, r, n).total : 0;
+}
+
+int moe_adapter_linear(const void *x_bf16, const void *w_bf16, const float *bias,
+                       const int32_t *adapter, const void *lora_a_bf16, const void *lora_b_bf16,
+                       const float *scale, int T, int din, int dout, int r, int n, void *y,
+                       int y_dtype, float *u_out, void *ws, size_t ws_bytes, void *stream)
+{
+    int rc = ad_check(T, din, dout, r, n);
+    if (rc != MOE_OK)
+        return rc;
+    if (y_dtype != MOE_DTYPE_F32 && y_dtype != MOE_DTYPE_BF16)
+        return MOE_ERR_INVALID_ARG;
+    if (T == 0)
+        return MOE_OK;
+    if (!x_bf16 || !adapter || !lora_a_bf16 || !lora_b_bf16 || !y || !aligned16(x_bf16) ||
+        !aligned16(w_bf16) || !aligned16(lora_a_bf16) || !aligned16(lora_b_bf16) || !aligned16(y) ||
+        !aligned16(u_out) || !aligned4(adapter) || !aligned4(scale) || !aligned4(bias))
+        return MOE_ERR_INVALID_ARG;
+    const AdLayout L = ad_layout(T, din, dout, r, n);
+    if ((rc = ad_check_ws(ws, ws_bytes, L.total)) != MOE_OK)
+        return rc;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    WsHeader *hdr = static_cast<WsHeader *>(ws);
+    float *u = u_out ? u_out : at<float>(ws, L.inner);
+    const uint16_t *x = static_cast<const uint16_t *>(x_bf16);
+    AdInnerArgs ai = {x, static_cast<const uint16_t *>(lora_a_bf16), adapter, scale, u, T, din, r, n,
+                      &hdr->status};
+    if ((rc = enqueue_ad_inner(ai, s)) != MOE_OK)
+        return rc;
+    AdProductArgs ap = {x, static_cast<const uint16_t *>(w_bf16), bias,
+                        static_cast<const uint16_t *>(lora_b_bf16), adapter, u, y,
+                        y_dtype == MOE_DTYPE_BF16, T, din, dout, r, n, &hdr->status};
+    return enqueue_ad_product(ap, s);
+}
+
+int moe_adapter_backward(const void *dy_bf16, const void *x_bf16, const void *w_t_bf16,
+                         const int32_t *adapter, const void *lora_a_bf16, const void *lora_b_bf16,
+                         const float *scale, const float *u, int T, int din, int dout, int r,
+                         int n, void *dx, int dx_dtype, float *d_lora_a, float *d_lora_b, void *ws,
+                         size_t ws_bytes, void *stream)
+{
+    int rc = ad_check(T, din, dout, r, n);
+    if (rc != MOE_OK)
+        return rc;
+    if (dx_dtype != MOE_DTYPE_F32 && dx_dtype != MOE_DTYPE_BF16)
+        return MOE_ERR_INVALID_ARG;
+    if (!aligned16(dx) || !aligned16(d_lora_a) || !aligned16(d_lora_b))
+        return MOE_ERR_INVALID_ARG;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (T == 0) {
+        if (d_lora_a && cudaMemsetAsync(d_lora_a, 0, sizeof(float) * (size_t)n * r * din, s) !=
+                            cudaSuccess)
+            return MOE_ERR_CUDA;
+        if (d_lora_b && cudaMemsetAsync(d_lora_b, 0, sizeof(float) * (size_t)n * r * dout, s) !=
+                            cudaSuccess)
+            return MOE_ERR_CUDA;
+        return MOE_OK;
+    }
+    if ((!dx && !d_lora_a && !d_lora_b) || !dy_bf16 || !adapter || (d_lora_a && !x_bf16) || (d_lora_b && !u) ||
+        ((dx || d_lora_a) && !lora_b_bf16) || (dx && !lora_a_bf16) || !aligned16(dy_bf16) ||
+        !aligned16(x_bf16) || !aligned16(w_t_bf16) || !aligned16(lora_a_bf16) ||
+        !aligned16(lora_b_bf16) || !aligned16(u) || !aligned4(adapter) || !aligned4(scale))
+        return MOE_ERR_INVALID_ARG;
+    const AdLayout L = ad_layout(T, din, dout, r, n);
+    if ((rc = ad_check_ws(ws, ws_bytes, L.total)) != MOE_OK)
+        return rc;
+    WsHeader *hdr = static_cast<WsHeader *>(ws);
+    float *v = at<float>(ws, L.inner);
+    const uint16_t *dy = static_cast<const uint16_t *>(dy_bf16);
+    const uint16_t *x = static_cast<const uint16_t *>(x_bf16);
+    if (dx || d_lora_a) {
+        AdInnerArgs ai = {dy, static_cast<const uint16_t *>(lora_b_bf16), adapter, scale, v, T, dout,
+                          r, n, &hdr->status};
+        if ((rc = enqueue_ad_inner(ai, s)) != MOE_OK)
+            return rc;
+    }
+    if (dx) {
+        AdProductArgs ap = {dy, static_cast<const uint16_t *>(w_t_bf16), nullptr,
+                            static_cast<const uint16_t *>(lora_a_bf16), adapter, v, dx,
+                            dx_dtype == MOE_DTYPE_BF16, T, dout, din, r, n, &hdr->status};
+        if ((rc = enqueue_ad_product(ap, s)) != MOE_OK)
+            return rc;
+    }
+    if (d_lora_a) {
+        AdOuterArgs ao = {v, x, adapter, d_lora_a, T, din, r, n, &hdr->status};
+        if ((rc = enqueue_ad_outer(ao, s)) != MOE_OK)
+            return rc;
+    }
+    if (d_lora_b) {
+        AdOuterArgs ao = {u, dy, adapter, d_lora_b, T, dout, r, n, &hdr->status};
+        if ((rc = enqueue_ad_outer(ao, s)) != MOE_OK)
+            return rc;
+    }
+    return MOE_OK;
+}
+
+}  // extern "C"
+
+// ========================================================================== router training
+namespace moe {
+
+struct BalLayout {
+    size_t p_acc, n_acc, arrive, z_part, total;
+};
+
+constexpr int kBalMaxGrid = 148 * 4;
+
+static BalLayout bal_layout(int E)
+{
+    BalLayout L;
+    size_t o = sizeof(WsHeader);
+    L.p_acc = o;   o = align256(o + sizeof(unsigned long long) * (size_t)E);
+    L.n_acc = o;   o = align256(o + sizeof(int32_t) * (size_t)(E + 1));
+    L.arrive = o;  o = align256(o + sizeof(unsigned));
+    L.z_part = o;  o = align256(o + sizeof(double) * kBalMaxGrid);
+    L.total = o;
+    return L;
+}
+
+static int bal_check(int T, int E, int k1)
+{
+    if (T < 0 || T > kMaxT || E < 1 || E > kMaxE)
+        return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (k1 < 1 || k1 > kMaxK1 || k1 > E)
+        return MOE_ERR_INVALID_ARG;
+    return MOE_OK;
+}
+
+// A row's values in a lane's registers: vectors of four where the rows keep
+// 16-byte alignment (E % 4 == 0), else single values.
+#define MOE_ROW_VARIANTS(CALL)                \
+    do {                                      \
+        if (E % 4 == 0) {                     \
+            if (E <= 128) { CALL(4, 4); }     \
+            if (E <= 256) { CALL(4, 8); }     \
+            if (E <= 512) { CALL(4, 16); }    \
+            CALL(4, 32);                      \
+        }                                     \
+        if (E <= 32) { CALL(1, 1); }          \
+        if (E <= 64) { CALL(1, 2); }          \
+        if (E <= 128) { CALL(1, 4); }         \
+        if (E <= 256) { CALL(1, 8); }         \
+        if (E <= 512) { CALL(1, 16); }        \
+        CALL(1, 32);                          \
+    } while (0)
+
+static int row_grid(int T)
+{
+    const int g = (T + kBalWarps - 1) / kBalWarps;
+    return g < kBalMaxGrid ? g : kBalMaxGrid;
+}
+
+static int enqueue_balance(const BalanceArgs &a, cudaStream_t s)
+{
+    const int E = a.E;
+#define MOE_BAL(VEC, N)                                                                        \
+    return launch(k_balance<VEC, N>, dim3(row_grid(a.T)), dim3(kBalWarps * 32),                \
+                  balance_smem_bytes(E), s, kPdl, a)
+    MOE_ROW_VARIANTS(MOE_BAL);
+#undef MOE_BAL
+}
+
+static int enqueue_route_backward(const RouteBackArgs &a, cudaStream_t s)
+{
+    const int E = a.E;
+#define MOE_RB(VEC, N)                                                                         \
+    return launch(k_route_backward<VEC, N>, dim3(row_grid(a.T)), dim3(kBalWarps * 32),         \
+                  route_backward_smem_bytes(E), s, kPdl, a)
+    MOE_ROW_VARIANTS(MOE_RB);
+#undef MOE_RB
+}
+
+}  // namespace moe
+
+extern "C" {
+
+size_t moe_balance_workspace_size(int T, int E)
+{
+    return bal_check(T, E, 1) == MOE_OK ? bal_layout(E).total : 0;
+}
+
+int moe_balance_loss(const float *logits, const int32_t *topk_idx, const unsigned char *token_mask,
+                     int T, int E, int k1, float balance_coef, float z_coef, int32_t *counts,
+                     float *loss, float *prob_mean, void *ws, size_t ws_bytes, void *stream)
+{
+    int rc = bal_check(T, E, k1);
+    if (rc != MOE_OK)
+        return rc;
+    if (!counts || !loss || !aligned4(counts) || !aligned4(loss) || !aligned4(prob_mean) ||
+        balance_coef != balance_coef || z_coef != z_coef)
+        return MOE_ERR_INVALID_ARG;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (T == 0) {
+        if (cudaMemsetAsync(counts, 0, sizeof(int32_t) * (E + 1), s) != cudaSuccess ||
+            cudaMemsetAsync(loss, 0, sizeof(float) * 3, s) != cudaSuccess ||
+            (prob_mean && cudaMemsetAsync(prob_mean, 0, sizeof(float) * E, s) != cudaSuccess))
+            return MOE_ERR_CUDA;
+        return MOE_OK;
+    }
+    if (!logits || !topk_idx || !aligned16(logits) || !aligned16(topk_idx))
+        return MOE_ERR_INVALID_ARG;
+    const BalLayout L = bal_layout(E);
+    if ((rc = ad_check_ws(ws, ws_bytes, L.total)) != MOE_OK)
+        return rc;
+    BalanceArgs a = {logits, topk_idx, token_mask, T, E, k1, balance_coef, z_coef, counts, loss,
+                     prob_mean, at<unsigned long long>(ws, L.p_acc), at<int>(ws, L.n_acc),
+                     at<unsigned>(ws, L.arrive), at<double>(ws, L.z_part),
+                     &static_cast<WsHeader *>(ws)->status};
+    return enqueue_balance(a, s);
+}
+
+int moe_route_backward(const float *logits, const int32_t *topk_idx, const float *d_topk_w,
+                       const int32_t *counts, const unsigned char *token_mask, int T, int E,
+                       int k1, int k2, float balance_coef, float z_coef, const float *d_loss,
+                       void *dlogits, int dz_dtype, void *ws, size_t ws_bytes, void *stream)
+{
+    int rc = bal_check(T, E, k1);
+    if (rc != MOE_OK)
+        return rc;
+    if (k2 < k1 || (dz_dtype != MOE_DTYPE_F32 && dz_dtype != MOE_DTYPE_BF16) ||
+        balance_coef != balance_coef || z_coef != z_coef)
+        return MOE_ERR_INVALID_ARG;
+    if (ws && ws_bytes < sizeof(WsHeader))
+        return MOE_ERR_WORKSPACE_TOO_SMALL;
+    if (T == 0)
+        return MOE_OK;
+    if (!logits || (!d_topk_w && !counts) || (d_topk_w && !topk_idx) || !dlogits || !aligned16(logits) ||
+        !aligned16(topk_idx) || !aligned16(dlogits) || !aligned4(d_topk_w) || !aligned4(counts) ||
+        !aligned4(d_loss) || (reinterpret_cast<uintptr_t>(ws) & 255))
+        return MOE_ERR_INVALID_ARG;
+    RouteBackArgs a = {logits, topk_idx, d_topk_w, counts, d_loss, token_mask, T, E, k1, k2,
+                       balance_coef, z_coef, dlogits, dz_dtype == MOE_DTYPE_BF16,
+                       ws ? &static_cast<WsHeader *>(ws)->status : nullptr};
+    return enqueue_route_backward(a, static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

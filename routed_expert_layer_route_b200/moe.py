@@ -71,6 +71,15 @@ SIGNATURES = {
     "moe_channel_norms": (_i, [_vp, _i, _i, _i, _i, _vp, _vp]),
     "moe_layer_channel_topk": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i,
                                     _vp, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "moe_adapter_workspace_size": (_sz, [_i, _i, _i, _i, _i]),
+    "moe_adapter_linear": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp, _i,
+                                _vp, _vp, _sz, _vp]),
+    "moe_adapter_backward": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp,
+                                  _i, _vp, _vp, _vp, _sz, _vp]),
+    "moe_balance_workspace_size": (_sz, [_i, _i]),
+    "moe_balance_loss": (_i, [_vp, _vp, _vp, _i, _i, _i, _f, _f, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "moe_route_backward": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _f, _f, _vp, _vp, _i, _vp,
+                                _sz, _vp]),
     "moe_test_exp_c": (_i, [_vp, _vp, ctypes.c_int64, _vp]),
     "moe_test_num_sms": (_i, []),
     "moe_test_set_grouped_single": (_i, [_i]),
@@ -394,3 +403,122 @@ def moe_layer_cascade(x, w_router, bias, w_gate, w_up, w_down, k1, k2, tau, y, w
                                    T, d, E, I, k1, k2, float(tau), _p(y), y_dtype, _p(topk_idx_out),
                                    _p(topk_w_out), _p(topk_count_out), _p(logits_out), flags, wsp,
                                    wsn, _stream(stream)), "moe_layer_cascade")
+
+
+_BF16 = (torch.bfloat16,)
+_F32 = (torch.float32,)
+_I32 = (torch.int32,)
+_OUT = (torch.float32, torch.bfloat16)
+_BYTE = (torch.bool, torch.uint8)
+
+
+def _given(where, device, *tensors):
+    """Each of (tensor or None, dtypes, shape) is dense, of one of these dtypes
+    and of this shape, on the current device; else MOE_ERR_INVALID_ARG."""
+    for t, dtypes, shape in tensors:
+        if t is not None and not (t.dtype in dtypes and t.shape == shape and t.is_contiguous()
+                                  and t.get_device() == device):
+            raise MoeError(MOE_ERR_INVALID_ARG, where)
+
+
+def _out_dtype(t):
+    return MOE_DTYPE_BF16 if t is not None and t.dtype == torch.bfloat16 else MOE_DTYPE_F32
+
+
+def moe_adapter_workspace_size(T, din, dout, r, n):
+    return lib().moe_adapter_workspace_size(T, din, dout, r, n)
+
+
+def adapter_workspace(T, din, dout, r, n, device=None, stream=None):
+    """Allocate (torch) and initialise a workspace for moe_adapter_linear and
+    moe_adapter_backward; streams as for workspace()."""
+    size = moe_adapter_workspace_size(T, din, dout, r, n)
+    if size == 0:
+        raise MoeError(MOE_ERR_UNSUPPORTED_SHAPE, "moe_adapter_workspace_size")
+    ws = torch.empty(size, dtype=torch.uint8, device=device or torch.device("cuda"))
+    moe_workspace_init(ws, stream)
+    return ws
+
+
+def moe_adapter_linear(x, w, bias, adapter, lora_a, lora_b, scale, y, ws, u_out=None, stream=None):
+    """y = x w^T + bias + each row's adapter: s (x A^T) B with A [n x r x din]
+    and B [n x r x dout] by rank; adapter [T] int32, MOE_EMPTY_SLOT for none.
+    w None: the adapters' part is added to y."""
+    T, din = x.shape
+    n, r, dout = lora_b.shape
+    _given("moe_adapter_linear", torch.cuda.current_device(), (x, _BF16, (T, din)),
+           (w, _BF16, (dout, din)), (bias, _F32, (dout,)), (adapter, _I32, (T,)),
+           (lora_a, _BF16, (n, r, din)), (lora_b, _BF16, (n, r, dout)), (scale, _F32, (n,)),
+           (y, _OUT, (T, dout)), (u_out, _F32, (T, r)))
+    wsp, wsn = _ws_args(ws)
+    _check(lib().moe_adapter_linear(_p(x), _p(w), _p(bias), _p(adapter), _p(lora_a), _p(lora_b),
+                                    _p(scale), T, din, dout, r, n, _p(y), _out_dtype(y), _p(u_out),
+                                    wsp, wsn, _stream(stream)), "moe_adapter_linear")
+
+
+def moe_adapter_backward(dy, x, w_t, adapter, lora_a, lora_b, scale, u, d_lora_a, d_lora_b, ws,
+                         dx=None, stream=None):
+    """Gradients of moe_adapter_linear: dx (None: left out) with w_t [din x
+    dout] (None: added to dx), d_lora_a and d_lora_b float32 (each nullable);
+    u as moe_adapter_linear's u_out."""
+    T, dout = dy.shape
+    n, r, din = lora_a.shape
+    _given("moe_adapter_backward", torch.cuda.current_device(), (dy, _BF16, (T, dout)),
+           (x, _BF16, (T, din)), (w_t, _BF16, (din, dout)), (adapter, _I32, (T,)),
+           (lora_a, _BF16, (n, r, din)), (lora_b, _BF16, (n, r, dout)), (scale, _F32, (n,)),
+           (u, _F32, (T, r)), (d_lora_a, _F32, (n, r, din)), (d_lora_b, _F32, (n, r, dout)),
+           (dx, _OUT, (T, din)))
+    wsp, wsn = _ws_args(ws)
+    _check(lib().moe_adapter_backward(_p(dy), _p(x), _p(w_t), _p(adapter), _p(lora_a), _p(lora_b),
+                                      _p(scale), _p(u), T, din, dout, r, n, _p(dx), _out_dtype(dx),
+                                      _p(d_lora_a), _p(d_lora_b), wsp, wsn, _stream(stream)),
+           "moe_adapter_backward")
+
+
+def moe_balance_workspace_size(T, E):
+    return lib().moe_balance_workspace_size(T, E)
+
+
+def balance_workspace(T, E, device=None, stream=None):
+    """Allocate (torch) and initialise a workspace for moe_balance_loss;
+    streams as for workspace()."""
+    size = moe_balance_workspace_size(T, E)
+    if size == 0:
+        raise MoeError(MOE_ERR_UNSUPPORTED_SHAPE, "moe_balance_workspace_size")
+    ws = torch.empty(size, dtype=torch.uint8, device=device or torch.device("cuda"))
+    moe_workspace_init(ws, stream)
+    return ws
+
+
+def moe_balance_loss(logits, topk_idx, balance_coef, z_coef, counts, loss, ws, token_mask=None,
+                     prob_mean=None, stream=None):
+    """counts [E + 1] int32 (slots per expert, then the counting tokens), loss
+    [3] = (weighted sum, balance loss, z loss) and prob_mean [E] of a route;
+    token_mask [T] bool or uint8, False for padding."""
+    T, E = logits.shape
+    k1 = topk_idx.shape[-1]
+    _given("moe_balance_loss", torch.cuda.current_device(), (logits, _F32, (T, E)),
+           (topk_idx, _I32, (T, k1)), (token_mask, _BYTE, (T,)), (counts, _I32, (E + 1,)),
+           (loss, _F32, (3,)), (prob_mean, _F32, (E,)))
+    wsp, wsn = _ws_args(ws)
+    _check(lib().moe_balance_loss(_p(logits), _p(topk_idx), _p(token_mask), T, E, k1,
+                                  float(balance_coef), float(z_coef), _p(counts), _p(loss),
+                                  _p(prob_mean), wsp, wsn, _stream(stream)), "moe_balance_loss")
+
+
+def moe_route_backward(logits, topk_idx, k2, d_topk_w, dlogits, counts=None, balance_coef=0.0,
+                       z_coef=0.0, d_loss=None, token_mask=None, ws=None, stream=None):
+    """dlogits from the routing weights' gradient d_topk_w (None: left out)
+    and, with counts from moe_balance_loss, from its losses (d_loss: device
+    float32 scalar, None for 1)."""
+    T, E = logits.shape
+    k1 = topk_idx.shape[-1]
+    _given("moe_route_backward", torch.cuda.current_device(), (logits, _F32, (T, E)),
+           (topk_idx, _I32, (T, k1)), (d_topk_w, _F32, (T, k1)), (counts, _I32, (E + 1,)),
+           (token_mask, _BYTE, (T,)), (dlogits, _OUT, (T, E)),
+           (d_loss, _F32, d_loss.shape if d_loss is not None and d_loss.numel() == 1 else None))
+    wsp, wsn = _ws_args(ws)
+    _check(lib().moe_route_backward(_p(logits), _p(topk_idx), _p(d_topk_w), _p(counts),
+                                    _p(token_mask), T, E, k1, k2, float(balance_coef),
+                                    float(z_coef), _p(d_loss), _p(dlogits), _out_dtype(dlogits),
+                                    wsp, wsn, _stream(stream)), "moe_route_backward")
