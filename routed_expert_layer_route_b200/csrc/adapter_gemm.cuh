@@ -1,0 +1,464 @@
+// adapter_gemm.cuh -- the shared projection with its adapters on the tensor
+// cores (tcgen05.mma on CTA pairs), for more rows than k_ad_rows takes.
+//
+//     Y [T x dout] = X W^T + sum over the adapters a of M_a U B_a
+//
+// with M_a the diagonal 0/1 matrix of the rows that are a's: the adapters'
+// part is a contraction over (adapter, rank) appended to the one over din, so
+// it lands in the same tensor-memory accumulator before the one store of y.
+// A tile of 256 rows takes only the adapters that occur in it.  Its U operand
+// is written by four warps of each CTA -- a row's own adapter's u, zeros for
+// the others -- in the two bf16 parts (hi, lo: u to 16 bits), its B operand
+// is a TMA copy of B_a as it lies in memory (16 ranks x outputs, the operand
+// whose rows run along N).  Each unit of 16 ranks costs two matrix
+// instructions where din costs din / 16, so one adapter of rank 16 in a tile
+// adds 2 to din / 16 instructions.
+//
+// Zeros do not silence a NaN or inf: 0 x inf is NaN, so a broken adapter
+// would reach the other rows of its tile.  Every such product is a NaN, so
+// the epilogue computes an output that came out NaN once more, alone, from
+// its own row and adapter.
+//
+// The two CTAs of a pair share tiles of 256 rows x BN outputs: each holds its
+// 128 rows of X and half of the outputs' rows of W in shared memory, and the
+// accumulators of its 128 rows (two sets of BN columns, so the epilogue of
+// one tile overlaps the next).  Tiles go to the pairs in turn, all column
+// blocks of a row block side by side in time.  Roles of a CTA's 448 threads:
+//   warps 0-3, 6-9  epilogue (two warps a quarter of the tensor-memory lanes)
+//   warp 4          TMA producer of X and W
+//   warp 5          tensor memory; in CTA 0 one thread issues the MMAs
+//   warps 10-13     the U operand, the list of a tile's adapters, TMA of B
+// X and W need nothing of the inner kernel and are loaded while it runs (it
+// lets this kernel start after its own wait); the U warps and the epilogue
+// wait for it.  Every wait is bounded, as in gemm_pair.cuh.
+#pragma once
+#include "adapter.cuh"
+#include "gemm_pair.cuh"
+
+namespace moe {
+
+constexpr int kAGRows = 256;    // rows of a pair's tile
+constexpr int kAGThreads = 448;
+constexpr int kAGWarpU = 10;    // first of the U warps
+constexpr int kAGEpiWarps = 8;
+constexpr int kAGUBufs = 2;     // U/B buffers, two units of 16 ranks each
+constexpr int kAGTileA = 128 * kGBK * 2;  // 16 KB: a CTA's rows of one K block
+
+template <int BN>
+struct AGShape {
+    static constexpr int kTileB = BN / 2 * kGBK * 2;     // a CTA's outputs of one K block
+    static constexpr int kStage = kAGTileA + kTileB;
+    static constexpr int kStages = BN == 256 ? 5 : 6;
+    static constexpr int kUnitB = BN / 2 * 16 * 2;       // a CTA's outputs of one unit
+    static constexpr int kUBuf = kAGTileA + 2 * kUnitB;
+};
+
+struct AGSync {
+    uint64_t full[6];             // CTA 0: both CTAs' tiles of stage s landed
+    uint64_t empty[6];            // each CTA: the MMAs reading stage s finished
+    uint64_t ufull[kAGUBufs];     // CTA 0: both CTAs' U warps and B copies are there
+    uint64_t uempty[kAGUBufs];    // each CTA: the MMAs reading the buffer finished
+    uint64_t acc_full[2];         // each CTA: accumulator set b is complete
+    uint64_t acc_empty[2];        // CTA 0: both epilogues have read set b
+    uint64_t drained;             // each CTA: every MMA has completed
+    uint64_t bye;                 // each CTA: the other CTA has finished
+    int u_units[kAGUBufs];        // units in the buffer, + 4: the tile's last buffer
+    uint32_t tmem_base;
+    int abort;
+    uint32_t bits[32];            // the adapters of a tile
+    uint16_t list[kAGRows];
+    int count;
+};
+
+template <int BN>
+inline size_t ag_smem_bytes()
+{
+    return 1024 + (size_t)AGShape<BN>::kStages * AGShape<BN>::kStage +
+           (size_t)kAGUBufs * AGShape<BN>::kUBuf + sizeof(AGSync);
+}
+
+// Operand whose rows run along N (N contiguous), 128-byte swizzle: blocks of
+// 64 N values x 8 K values (8 rows of 128 bytes); lbo from 64 values of N to
+// the next, 1024 bytes from 8 values of K to the next.
+MOE_DEVINL uint64_t umma_desc_mn_sw128(uint32_t saddr, uint32_t lbo)
+{
+    return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)(lbo >> 4) << 16) |
+           ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
+MOE_DEVINL void tma_load_3d_pair(void *dst, const CUtensorMap *map, int x, int y, int z,
+                                 uint32_t bar_caddr)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_addr(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_caddr), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+
+// Bytes that the current phase of `bar` still waits for, without an arrival.
+MOE_DEVINL void mbar_expect_tx(uint64_t *bar, uint32_t bytes)
+{
+    asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(bar)),
+                 "r"(bytes)
+                 : "memory");
+}
+
+MOE_DEVINL bool ag_aborted(const AGSync &sy) { return *(volatile const int *)&sy.abort != 0; }
+
+// One output alone, in float32: the row's product with W (or what y holds)
+// and its own adapter's part.
+__device__ __noinline__ float ag_one(const AdProductArgs &p, int a, int t, int o)
+{
+    float v = 0.0f;
+    if (p.w) {
+        const uint16_t *x = p.x + (size_t)t * p.din, *w = p.w + (size_t)o * p.din;
+        for (int k = 0; k < p.din; k += 8) {
+            const uint4 a8 = __ldg(reinterpret_cast<const uint4 *>(x + k));
+            const float xv[8] = {bf16lo(a8.x), bf16hi(a8.x), bf16lo(a8.y), bf16hi(a8.y),
+                                 bf16lo(a8.z), bf16hi(a8.z), bf16lo(a8.w), bf16hi(a8.w)};
+            v = dot8_bf16(__ldg(reinterpret_cast<const uint4 *>(w + k)), xv, v);
+        }
+    }
+    return a >= 0 ? v + ad_part(p, a, t, o) : v;
+}
+
+template <int BN>
+__global__ void __launch_bounds__(kAGThreads, 1)
+    k_ad_gemm(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
+              const __grid_constant__ CUtensorMap tm_b, AdProductArgs p)
+{
+    using S = AGShape<BN>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *ring = g_align1024(smem_raw);
+    uint8_t *ubuf = ring + (size_t)S::kStages * S::kStage;
+    AGSync &sy = *reinterpret_cast<AGSync *>(ubuf + (size_t)kAGUBufs * S::kUBuf);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t rank = cluster_rank(), peer = rank ^ 1u;
+    const bool lead = rank == 0;
+    int *status = &p.hdr->status;
+
+    if (tid == 0) {
+        for (int s = 0; s < S::kStages; ++s) {
+            mbar_init(&sy.full[s], 1);
+            mbar_init(&sy.empty[s], 1);
+        }
+        for (int b = 0; b < kAGUBufs; ++b) {
+            mbar_init(&sy.ufull[b], 8);  // four U warps of each CTA
+            mbar_init(&sy.uempty[b], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&sy.acc_full[b], 1);
+            mbar_init(&sy.acc_empty[b], 2 * kAGEpiWarps);
+        }
+        mbar_init(&sy.drained, 1);
+        mbar_init(&sy.bye, 1);
+        sy.abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == kGWarpMma) {
+        tmem_alloc_pair(&sy.tmem_base, 2 * BN);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();
+    tc_fence_after();
+    const uint32_t tmem = sy.tmem_base;
+
+    const int nkb = p.w ? (p.din + kGBK - 1) / kGBK : 0;
+    const int ncol = (p.dout + BN - 1) / BN, nrow = (p.T + kAGRows - 1) / kAGRows;
+    const int tiles = nrow * ncol, pairs = gridDim.x / 2, pair = blockIdx.x / 2;
+    const int nch = ad_rp(p.r) / 16;  // units of an adapter
+
+    if (warp == kGWarpTma) {
+        if (lane == 0) {
+            uint32_t g = 0;
+            for (int i = pair; i < tiles && !ag_aborted(sy); i += pairs) {
+                const int t0 = i / ncol * kAGRows + (int)rank * 128;
+                const int o0 = i % ncol * BN + (int)rank * (BN / 2);
+                for (int kb = 0; kb < nkb; ++kb, ++g) {
+                    const int s = g % S::kStages;
+                    if (!mbar_wait_cluster(&sy.empty[s], ((g / S::kStages) & 1) ^ 1, status)) {
+                        sy.abort = 1;
+                        break;
+                    }
+                    uint8_t *st = ring + (size_t)s * S::kStage;
+                    const uint32_t fb = cluster_addr(&sy.full[s], 0);
+                    if (lead)  // both CTAs' bytes
+                        mbar_arrive_expect_tx(&sy.full[s], 2 * S::kStage);
+                    tma_load_2d_pair(st, &tm_x, kb * kGBK, t0, fb);
+                    tma_load_2d_pair(st + kAGTileA, &tm_w, kb * kGBK, o0, fb);
+                }
+            }
+            // CTA 0: every stage issued has landed before the CTA may leave
+            if (lead)
+                for (uint32_t r = g > (uint32_t)S::kStages ? g - S::kStages : 0; r < g; ++r)
+                    mbar_wait(&sy.full[r % S::kStages], (r / S::kStages) & 1, status);
+        }
+    } else if (warp == kGWarpMma) {
+        if (lane == 0 && lead) {
+            uint32_t g = 0, ub = 0, itc = 0;
+            const uint32_t idesc = umma_idesc_bf16(kAGRows, BN);
+            const uint32_t idesc_mn = idesc | (1u << 16);  // B along N
+            for (int i = pair; i < tiles; i += pairs, ++itc) {
+                const int buf = itc & 1;
+                if (!mbar_wait_cluster(&sy.acc_empty[buf], ((itc >> 1) & 1) ^ 1, status)) {
+                    sy.abort = 1;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t dt = tmem + buf * BN;
+                uint32_t acc = 0;
+                for (int kb = 0; kb < nkb; ++kb, ++g) {
+                    const int s = g % S::kStages;
+                    if (!mbar_wait_cluster(&sy.full[s], (g / S::kStages) & 1, status)) {
+                        sy.abort = 1;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t st = smem_addr(ring + (size_t)s * S::kStage);
+#pragma unroll
+                    for (int kk = 0; kk < kGBK / 16; ++kk) {
+                        umma_bf16_pair(dt, umma_desc_sw128(st + kk * 32),
+                                       umma_desc_sw128(st + kAGTileA + kk * 32), idesc, acc);
+                        acc = 1;
+                    }
+                    umma_commit_pair_both(&sy.empty[s]);
+                }
+                while (!ag_aborted(sy)) {
+                    const int b = ub % kAGUBufs;
+                    if (!mbar_wait_cluster(&sy.ufull[b], (ub / kAGUBufs) & 1, status)) {
+                        sy.abort = 1;
+                        break;
+                    }
+                    tc_fence_after();
+                    const int units = *(volatile int *)&sy.u_units[b];
+                    const uint32_t st = smem_addr(ubuf + (size_t)b * S::kUBuf);
+                    for (int k = 0; k < (units & 3); ++k) {
+                        const uint64_t bd =
+                            umma_desc_mn_sw128(st + kAGTileA + k * S::kUnitB, 2048);
+                        umma_bf16_pair(dt, umma_desc_sw128(st + k * 64), bd, idesc_mn, acc);
+                        umma_bf16_pair(dt, umma_desc_sw128(st + k * 64 + 32), bd, idesc_mn, 1);
+                        acc = 1;
+                    }
+                    umma_commit_pair_both(&sy.uempty[b]);
+                    ++ub;
+                    if (units & 4)
+                        break;
+                }
+                if (ag_aborted(sy))
+                    break;
+                umma_commit_pair_both(&sy.acc_full[buf]);
+            }
+            umma_commit_pair_both(&sy.drained);
+            mbar_wait(&sy.drained, 0, status);
+        }
+    } else if (warp >= kAGWarpU) {
+        // ------------------------------------------------------------ U and B
+        const int ut = tid - kAGWarpU * 32;  // this CTA's row of the tile
+        const int rp = ad_rp(p.r);
+        uint32_t ub = 0;
+        pdl_wait();
+        for (int i = pair; i < tiles; i += pairs) {
+            // the tile's adapters, both CTAs' rows, in order of their number
+            const int tb = i / ncol * kAGRows;
+            const int t = tb + (int)rank * 128 + ut, tp = tb + (int)peer * 128 + ut;
+            const int a = t < p.T ? adapter_of(p.adapter, t, p.n, status) : -1;
+            const int ap = tp < p.T ? adapter_of(p.adapter, tp, p.n, status) : -1;
+            if (ut < 32)
+                sy.bits[ut] = 0u;
+            named_bar_sync(1, 128);
+            if (a >= 0)
+                atomicOr(&sy.bits[a >> 5], 1u << (a & 31));
+            if (ap >= 0)
+                atomicOr(&sy.bits[ap >> 5], 1u << (ap & 31));
+            named_bar_sync(1, 128);
+            if (ut < 32) {
+                uint32_t w = sy.bits[ut];
+                int at = __popc(w), n = at;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int v = __shfl_up_sync(0xffffffffu, at, o);
+                    if (ut >= o)
+                        at += v;
+                }
+                int total = __shfl_sync(0xffffffffu, at, 31);
+                at -= n;
+                while (w) {
+                    sy.list[at++] = (uint16_t)(ut * 32 + __ffs(w) - 1);
+                    w &= w - 1;
+                }
+                // nothing to add and no product: one unit of zeros fills the accumulators
+                if (total == 0 && !p.w) {
+                    total = 1;
+                    if (ut == 0)
+                        sy.list[0] = 0;
+                }
+                if (ut == 0)
+                    sy.count = total;
+            }
+            named_bar_sync(1, 128);
+            const int units = sy.count * nch;
+            const int o0 = i % ncol * BN + (int)rank * (BN / 2);
+            const uint16_t *urow = p.parts + (size_t)(a >= 0 ? t : 0) * 2 * rp;
+            int u0 = 0;
+            do {
+                const int b = ub % kAGUBufs, nu = min(2, units - u0);
+                // one lane waits for its warp
+                int ok = 1;
+                if (lane == 0)
+                    ok = mbar_wait_cluster(&sy.uempty[b], ((ub / kAGUBufs) & 1) ^ 1, status);
+                if (!__shfl_sync(0xffffffffu, ok, 0)) {
+                    sy.abort = 1;
+                    break;
+                }
+                uint8_t *st = ubuf + (size_t)b * S::kUBuf;
+                if (ut == 0) {
+                    if (lead)
+                        sy.u_units[b] = nu | (u0 + 2 >= units ? 4 : 0);
+                    const uint32_t fb = cluster_addr(&sy.ufull[b], 0);
+                    if (lead && nu > 0)
+                        mbar_expect_tx(&sy.ufull[b], 2 * nu * S::kUnitB);
+                    for (int k = 0; k < nu; ++k) {
+                        const int e = sy.list[(u0 + k) / nch], j = (u0 + k) % nch * 16;
+                        for (int c = 0; c < BN / 128; ++c)
+                            tma_load_3d_pair(st + kAGTileA + k * S::kUnitB + c * 2048, &tm_b,
+                                             o0 + 64 * c, j, e, fb);
+                    }
+                }
+                for (int k = 0; k < nu; ++k) {
+                    const int e = sy.list[(u0 + k) / nch], j = (u0 + k) % nch * 16;
+                    uint4 v[4] = {};
+                    if (a == e) {
+                        const uint4 *h = reinterpret_cast<const uint4 *>(urow + j);
+                        const uint4 *l = reinterpret_cast<const uint4 *>(urow + rp + j);
+                        v[0] = __ldcg(h);
+                        v[1] = __ldcg(h + 1);
+                        v[2] = __ldcg(l);
+                        v[3] = __ldcg(l + 1);
+                    }
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        *reinterpret_cast<uint4 *>(st + ut * 128 +
+                                                   (((k * 4 + c) ^ (ut & 7)) << 4)) = v[c];
+                }
+                asm volatile("fence.proxy.async;" ::: "memory");
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive_cluster(cluster_addr(&sy.ufull[b], 0));
+                ++ub;
+                u0 += 2;
+            } while (u0 < units);
+            named_bar_sync(1, 128);  // the list has been read; all four warps see an abort
+            if (ag_aborted(sy))
+                break;
+        }
+    } else {
+        // ------------------------------------------------------------ epilogue
+        const int lq = warp & 3, eh = warp >= 6;
+        const uint32_t lane_addr = tmem + ((uint32_t)(lq * 32) << 16);
+        uint32_t itc = 0;
+        pdl_wait();
+        for (int i = pair; i < tiles; i += pairs, ++itc) {
+            const int buf = itc & 1;
+            const int t = i / ncol * kAGRows + (int)rank * 128 + lq * 32 + lane;
+            const int o0 = i % ncol * BN;
+            int ok = 1;
+            if (lane == 0)
+                ok = mbar_wait_cluster(&sy.acc_full[buf], (itc >> 1) & 1, status);
+            if (!__shfl_sync(0xffffffffu, ok, 0)) {
+                sy.abort = 1;
+                break;
+            }
+            tc_fence_after();
+            const int a = t < p.T ? adapter_of(p.adapter, t, p.n, nullptr) : -1;
+#pragma unroll 1
+            for (int c = eh; c < BN / 32; c += 2) {
+                const int o = o0 + c * 32;
+                if (o >= p.dout)
+                    break;
+                float v[32];
+                __syncwarp();
+                tmem_ld32(lane_addr + buf * BN + c * 32, v);
+                if (t >= p.T)
+                    continue;
+                bool bad = false;
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    bad |= v[j] != v[j];
+                if (bad)
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (v[j] != v[j] && o + j < p.dout)
+                            v[j] = ag_one(p, a, t, o + j);
+                const size_t at = (size_t)t * p.dout + o;
+                // dout % 8 == 0: vectors of eight outputs are whole or absent
+#pragma unroll
+                for (int j = 0; j < 32; j += 8) {
+                    if (o + j >= p.dout)
+                        break;
+                    if (p.bias) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            v[j + k] += __ldg(&p.bias[o + j + k]);
+                    }
+                    if (p.y_bf16) {
+                        uint4 *y = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.y) + at + j);
+                        if (!p.w) {
+                            const uint4 old = *y;
+                            v[j] += bf16lo(old.x);
+                            v[j + 1] += bf16hi(old.x);
+                            v[j + 2] += bf16lo(old.y);
+                            v[j + 3] += bf16hi(old.y);
+                            v[j + 4] += bf16lo(old.z);
+                            v[j + 5] += bf16hi(old.z);
+                            v[j + 6] += bf16lo(old.w);
+                            v[j + 7] += bf16hi(old.w);
+                        }
+                        *y = make_uint4(pack_bf16x2(v[j], v[j + 1]), pack_bf16x2(v[j + 2], v[j + 3]),
+                                        pack_bf16x2(v[j + 4], v[j + 5]),
+                                        pack_bf16x2(v[j + 6], v[j + 7]));
+                    } else {
+                        float4 *y = reinterpret_cast<float4 *>(static_cast<float *>(p.y) + at + j);
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            float4 n = make_float4(v[j + 4 * k], v[j + 4 * k + 1], v[j + 4 * k + 2],
+                                                   v[j + 4 * k + 3]);
+                            if (!p.w) {
+                                const float4 old = y[k];
+                                n.x += old.x;
+                                n.y += old.y;
+                                n.z += old.z;
+                                n.w += old.w;
+                            }
+                            y[k] = n;
+                        }
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive_cluster(cluster_addr(&sy.acc_empty[buf], 0));
+        }
+    }
+    // tensor memory goes back once every MMA has completed, and neither CTA's
+    // shared memory goes away while the other may still reach it
+    tc_fence_before();
+    __syncthreads();
+    pdl_trigger();
+    if (warp == kGWarpMma) {
+        if (lane == 0 && !lead)
+            mbar_wait(&sy.drained, 0, status);
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, 2 * BN);
+    }
+    if (tid == 0) {
+        mbar_arrive_cluster(cluster_addr(&sy.bye, peer));
+        mbar_wait_cluster(&sy.bye, 0, status);
+    }
+}
+
+}  // namespace moe

@@ -12,6 +12,7 @@
 #include "../../include/moe.h"
 #include "../../include/moe_testing.h"
 #include "adapter.cuh"
+#include "adapter_gemm.cuh"
 #include "balance.cuh"
 #include "combine.cuh"
 #include "ctopk.cuh"
@@ -102,6 +103,7 @@ struct DevInfo {
     bool ready = false;
     int num_sms = 0;
     int gemm1_pairs = 0;  // CTA pairs of k_gemm1_pair resident at once (0: not launchable)
+    int ad_pairs = 0;     // CTA pairs of k_ad_gemm
 };
 
 // Which grouped GEMM kernels the grouped path uses (test hook): 0 the pair
@@ -178,6 +180,13 @@ static int device_info(DevInfo *&out)
         // scores of kCtkMaxN channels + at most 16 KiB of side-by-side row partials
         if (cudaFuncSetAttribute(k_ctk_down, dsm, kCtkMaxN * 4 + 16 * 1024) != cudaSuccess)
             return MOE_ERR_CUDA;
+        if (cudaFuncSetAttribute(k_ad_gemm<256>, dsm, (int)ag_smem_bytes<256>()) != cudaSuccess ||
+            cudaFuncSetAttribute(k_ad_gemm<128>, dsm, (int)ag_smem_bytes<128>()) != cudaSuccess ||
+            cudaFuncSetAttribute(k_ad_outer<1>, dsm, AdOuterSmem<1>::kBytes) != cudaSuccess ||
+            cudaFuncSetAttribute(k_ad_outer<2>, dsm, AdOuterSmem<2>::kBytes) != cudaSuccess ||
+            cudaFuncSetAttribute(k_ad_outer<4>, dsm, AdOuterSmem<4>::kBytes) != cudaSuccess)
+            return MOE_ERR_CUDA;
+        di.ad_pairs = pair_occupancy(k_ad_gemm<256>, kAGThreads, ag_smem_bytes<256>(), di.num_sms);
         const int small = 96 * 1024;
         if (cudaFuncSetAttribute(k_logits, cudaFuncAttributeMaxDynamicSharedMemorySize, small) !=
                 cudaSuccess ||
@@ -1508,17 +1517,47 @@ namespace moe {
 constexpr int kAdMaxDim = 16384, kAdMaxR = 128, kAdMaxN = 1024;
 
 struct AdLayout {
-    size_t inner, total;
+    size_t parts, given, offsets, row, pos, hist, arrive, partial, total;
 };
+
+static int ad_col_blocks(int D) { return (D + kAdOutCols - 1) / kAdOutCols; }
+// 16-rank tiles of an outer-product CTA, and its blocks of ranks
+static int ad_mt(int r) { return r <= 16 ? 1 : r <= 32 ? 2 : 4; }
+static int ad_rank_blocks(int r) { return (r + 16 * ad_mt(r) - 1) / (16 * ad_mt(r)); }
+
+// Outer products: rows of one piece.  One adapter may hold all rows, so a
+// column block's rows are cut into enough pieces that the CTAs of one adapter
+// fill the device about twice; a piece has 64 rows at least.
+constexpr int kAdOutTarget = 2 * 148;
+
+static int ad_piece_rows(int T, int blocks)
+{
+    const int pieces = (kAdOutTarget + blocks - 1) / blocks;
+    const int rows = ((T + pieces - 1) / pieces + kAdOutRows - 1) / kAdOutRows * kAdOutRows;
+    return rows < 64 ? 64 : rows;
+}
 
 static AdLayout ad_layout(int T, int din, int dout, int r, int n)
 {
-    (void)din;
-    (void)dout;
-    (void)n;
     AdLayout L;
     size_t o = sizeof(WsHeader);
-    L.inner = o;   o = align256(o + sizeof(float) * (size_t)T * r);
+    const size_t rows = (size_t)T;
+    const size_t rp = (size_t)((r + 15) & ~15), both = (size_t)r * (din + dout);
+    L.parts = o;    o = align256(o + 4 * rows * rp);
+    L.given = o;    o = align256(o + 4 * rows * rp);
+    L.offsets = o;  o = align256(o + sizeof(int32_t) * (size_t)(n + 1));
+    L.row = o;      o = align256(o + sizeof(int32_t) * rows);
+    L.pos = o;      o = align256(o + sizeof(int32_t) * rows);
+    L.hist = o;     o = align256(o + sizeof(int32_t) * (size_t)perm_chunks(T) * n);
+    L.arrive = o;
+    o = align256(o + sizeof(int32_t) * (size_t)n * (ad_col_blocks(din) + ad_col_blocks(dout)) *
+                         ad_rank_blocks(r));
+    // scratch pieces: an adapter of len > rows has at most 2 len / rows, so all
+    // have at most 2 T / rows -- T / 32, and twice the pieces ad_piece_rows
+    // aims at, where blocks x 128 x 64 values at most make one
+    const size_t few = sizeof(float) * (rows / 32) * both;
+    const size_t many = sizeof(float) * 2 * ((size_t)kAdOutTarget * kAdOutCols * 64 + both);
+    L.partial = o;  o = align256(o + (few < many ? few : many));
     L.total = o;
     return L;
 }
@@ -1541,20 +1580,97 @@ static int ad_check_ws(const void *ws, size_t ws_bytes, size_t need)
     return ws_bytes < need ? MOE_ERR_WORKSPACE_TOO_SMALL : MOE_OK;
 }
 
-static int enqueue_ad_inner(AdInnerArgs a, cudaStream_t s)
+// Inner products (and, with conv or zero_n, CTAs behind them for those).
+static int enqueue_ad_inner(AdInnerArgs a, bool inner, cudaStream_t s)
 {
-    const int64_t items = (int64_t)a.T * a.r;
-    return launch(k_ad_inner, dim3((unsigned)((items + 7) / 8)), dim3(256), 0, s, kPdl, a);
+    const int tiles = (a.T + kAdTile - 1) / kAdTile;
+    // CTAs that share a tile's adapters: 16 where the tiles alone leave the
+    // device empty, fewer as they fill it
+    int lists = 2 * 148 / tiles;
+    a.lists = lists < 1 ? 1 : lists > kAdTile ? kAdTile : lists;
+    a.inner_ctas = inner ? tiles * a.lists : 0;
+    const int rp = (a.r + 15) & ~15;
+    const int64_t vals = a.conv ? (int64_t)a.T * rp : a.zero_n;
+    int64_t extra = (vals + 2047) / 2048;
+    if (extra > 148)
+        extra = 148;
+    if (a.inner_ctas + extra == 0)
+        return MOE_OK;
+    const unsigned gx = (unsigned)(a.inner_ctas + extra);
+    const dim3 block(kAdWarps * 32);
+    // ranks of a CTA: 16 while the rows are few and CTAs would idle, else up to 64
+    if (rp <= 16 || a.T <= kAdRows)
+        return launch(k_ad_inner<2>, dim3(gx, (rp + 15) / 16), block, 0, s, kPdl, a);
+    if (rp <= 32)
+        return launch(k_ad_inner<4>, dim3(gx, 1), block, 0, s, kPdl, a);
+    return launch(k_ad_inner<8>, dim3(gx, (rp + 63) / 64), block, 0, s, kPdl, a);
+}
+
+// [n x r x cols] bf16 read in boxes of 64 columns x 16 ranks, zeros behind r.
+static int rank_tile_map(CUtensorMap *m, const void *base, uint64_t cols, uint64_t r, uint64_t n)
+{
+    EncodeTiledFn enc = encode_tiled_fn();
+    if (!enc)
+        return MOE_ERR_CUDA;
+    const cuuint64_t dims[3] = {cols, r, n};
+    const cuuint64_t strides[2] = {cols * 2, cols * r * 2};
+    const cuuint32_t box[3] = {64, 16, 1};
+    const cuuint32_t es[3] = {1, 1, 1};
+    const CUresult rc = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims,
+                            strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return rc == CUDA_SUCCESS ? MOE_OK : MOE_ERR_CUDA;
 }
 
 static int enqueue_ad_product(AdProductArgs a, cudaStream_t s)
 {
-    return launch(k_ad_product, dim3((a.dout + 63) / 64, (a.T + 63) / 64), dim3(256), 0, s, kPdl, a);
+    if (a.T <= kAdRows) {
+        const dim3 block(kAdWarps * 32), grid((a.dout + 15) / 16);
+        if (a.T <= 8)
+            return launch(k_ad_rows<1>, grid, block, 0, s, kPdl, a);
+        if (a.T <= 16)
+            return launch(k_ad_rows<2>, grid, block, 0, s, kPdl, a);
+        if (a.T <= 32)
+            return launch(k_ad_rows<4>, grid, block, 0, s, kPdl, a);
+        return launch(k_ad_rows<8>, grid, block, 0, s, kPdl, a);
+    }
+    DevInfo *di;
+    int rc;
+    if ((rc = device_info(di)) != MOE_OK)
+        return rc;
+    if (di->ad_pairs < 1)
+        return MOE_ERR_CUDA;
+    const int rows = (a.T + kAGRows - 1) / kAGRows;
+    const bool wide = rows * ((a.dout + 255) / 256) >= di->ad_pairs;
+    const int bn = wide ? 256 : 128;
+    CUtensorMap tx, tw, tb;
+    if ((rc = rank_tile_map(&tb, a.b, a.dout, a.r, a.n)) != MOE_OK)
+        return rc;
+    tx = tw = tb;  // not read without w
+    if (a.w && ((rc = bf16_tile_map(&tx, a.x, a.din, a.T, 128)) != MOE_OK ||
+                (rc = bf16_tile_map(&tw, a.w, a.din, a.dout, bn / 2)) != MOE_OK))
+        return rc;
+    const int tiles = rows * ((a.dout + bn - 1) / bn);
+    const dim3 grid(2 * (tiles < di->ad_pairs ? tiles : di->ad_pairs));
+    if (wide)
+        return launch(k_ad_gemm<256>, grid, dim3(kAGThreads), ag_smem_bytes<256>(), s,
+                      kPdl | kPair, tx, tw, tb, a);
+    return launch(k_ad_gemm<128>, grid, dim3(kAGThreads), ag_smem_bytes<128>(), s, kPdl | kPair, tx,
+                  tw, tb, a);
 }
 
 static int enqueue_ad_outer(AdOuterArgs a, cudaStream_t s)
 {
-    return launch(k_ad_outer, dim3((a.D + 127) / 128, a.r, a.n), dim3(128), 0, s, kPdl, a);
+    const int mt = ad_mt(a.r), rb = ad_rank_blocks(a.r);
+    a.dch0 = a.pr[0].g ? ad_col_blocks(a.pr[0].D) : 0;
+    const int cols = a.dch0 + (a.pr[1].g ? ad_col_blocks(a.pr[1].D) : 0);
+    const dim3 grid(a.T / a.rows + a.n, cols, rb), block(256);
+    if (mt == 1)
+        return launch(k_ad_outer<1>, grid, block, AdOuterSmem<1>::kBytes, s, kPdl, a);
+    if (mt == 2)
+        return launch(k_ad_outer<2>, grid, block, AdOuterSmem<2>::kBytes, s, kPdl, a);
+    return launch(k_ad_outer<4>, grid, block, AdOuterSmem<4>::kBytes, s, kPdl, a);
 }
 
 }  // namespace moe
@@ -1587,15 +1703,27 @@ int moe_adapter_linear(const void *x_bf16, const void *w_bf16, const float *bias
         return rc;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     WsHeader *hdr = static_cast<WsHeader *>(ws);
-    float *u = u_out ? u_out : at<float>(ws, L.inner);
+    DevInfo *di;
+    if ((rc = device_info(di)) != MOE_OK)
+        return rc;
     const uint16_t *x = static_cast<const uint16_t *>(x_bf16);
-    AdInnerArgs ai = {x, static_cast<const uint16_t *>(lora_a_bf16), adapter, scale, u, T, din, r, n,
-                      &hdr->status};
-    if ((rc = enqueue_ad_inner(ai, s)) != MOE_OK)
+    AdInnerArgs ai = {};
+    ai.x = x;
+    ai.a = static_cast<const uint16_t *>(lora_a_bf16);
+    ai.adapter = adapter;
+    ai.scale = scale;
+    ai.parts = at<uint16_t>(ws, L.parts);
+    ai.u_out = u_out;
+    ai.T = T;
+    ai.din = din;
+    ai.r = r;
+    ai.n = n;
+    ai.status = &hdr->status;
+    if ((rc = enqueue_ad_inner(ai, true, s)) != MOE_OK)
         return rc;
     AdProductArgs ap = {x, static_cast<const uint16_t *>(w_bf16), bias,
-                        static_cast<const uint16_t *>(lora_b_bf16), adapter, u, y,
-                        y_dtype == MOE_DTYPE_BF16, T, din, dout, r, n, &hdr->status};
+                        static_cast<const uint16_t *>(lora_b_bf16), adapter, ai.parts, y,
+                        y_dtype == MOE_DTYPE_BF16, T, din, dout, r, n, hdr};
     return enqueue_ad_product(ap, s);
 }
 
@@ -1631,33 +1759,64 @@ int moe_adapter_backward(const void *dy_bf16, const void *x_bf16, const void *w_
     if ((rc = ad_check_ws(ws, ws_bytes, L.total)) != MOE_OK)
         return rc;
     WsHeader *hdr = static_cast<WsHeader *>(ws);
-    float *v = at<float>(ws, L.inner);
+    DevInfo *di;
+    if ((rc = device_info(di)) != MOE_OK)
+        return rc;
     const uint16_t *dy = static_cast<const uint16_t *>(dy_bf16);
     const uint16_t *x = static_cast<const uint16_t *>(x_bf16);
-    if (dx || d_lora_a) {
-        AdInnerArgs ai = {dy, static_cast<const uint16_t *>(lora_b_bf16), adapter, scale, v, T, dout,
-                          r, n, &hdr->status};
-        if ((rc = enqueue_ad_inner(ai, s)) != MOE_OK)
+    int32_t *offsets = at<int32_t>(ws, L.offsets), *row = at<int32_t>(ws, L.row);
+    const bool outer = d_lora_a || d_lora_b;
+    if (outer) {
+        // rows grouped by adapter: the counting sort of the routed slots, one slot a row
+        PermOut po = {offsets, row, at<int32_t>(ws, L.pos), nullptr, nullptr};
+        rc = T > 4096 ? enqueue_perm_parallel(adapter, T, 1, n, at<int>(ws, L.hist), po,
+                                              &hdr->status, s)
+                      : launch(k_permute, dim3(1), dim3(1024), permute_smem_bytes(n, T), s, kPdl,
+                               adapter, T, 1, n, po, &hdr->status);
+        if (rc != MOE_OK)
             return rc;
     }
+    const int cols = (d_lora_a ? ad_col_blocks(din) : 0) + (d_lora_b ? ad_col_blocks(dout) : 0);
+    AdInnerArgs ai = {};
+    ai.x = dy;
+    ai.a = static_cast<const uint16_t *>(lora_b_bf16);
+    ai.adapter = adapter;
+    ai.scale = scale;
+    ai.parts = at<uint16_t>(ws, L.parts);
+    ai.conv = d_lora_b ? u : nullptr;
+    ai.conv_parts = at<uint16_t>(ws, L.given);
+    ai.zero = at<int>(ws, L.arrive);
+    ai.zero_n = outer ? n * cols * ad_rank_blocks(r) : 0;
+    ai.T = T;
+    ai.din = dout;
+    ai.r = r;
+    ai.n = n;
+    ai.status = &hdr->status;
+    if ((rc = enqueue_ad_inner(ai, dx || d_lora_a, s)) != MOE_OK)
+        return rc;
     if (dx) {
         AdProductArgs ap = {dy, static_cast<const uint16_t *>(w_t_bf16), nullptr,
-                            static_cast<const uint16_t *>(lora_a_bf16), adapter, v, dx,
-                            dx_dtype == MOE_DTYPE_BF16, T, dout, din, r, n, &hdr->status};
+                            static_cast<const uint16_t *>(lora_a_bf16), adapter, ai.parts, dx,
+                            dx_dtype == MOE_DTYPE_BF16, T, dout, din, r, n, hdr};
         if ((rc = enqueue_ad_product(ap, s)) != MOE_OK)
             return rc;
     }
-    if (d_lora_a) {
-        AdOuterArgs ao = {v, x, adapter, d_lora_a, T, din, r, n, &hdr->status};
-        if ((rc = enqueue_ad_outer(ao, s)) != MOE_OK)
-            return rc;
-    }
-    if (d_lora_b) {
-        AdOuterArgs ao = {u, dy, adapter, d_lora_b, T, dout, r, n, &hdr->status};
-        if ((rc = enqueue_ad_outer(ao, s)) != MOE_OK)
-            return rc;
-    }
-    return MOE_OK;
+    if (!outer)
+        return MOE_OK;
+    AdOuterArgs ao = {};
+    ao.pr[0] = {ai.parts, x, d_lora_a, din};
+    ao.pr[1] = {ai.conv_parts, dy, d_lora_b, dout};
+    ao.offsets = offsets;
+    ao.row = row;
+    ao.partial = at<float>(ws, L.partial);
+    ao.arrive = ai.zero;
+    // the same pieces whichever outputs are asked for, so that they do not change the sums
+    ao.rows = ad_piece_rows(T, (ad_col_blocks(din) + ad_col_blocks(dout)) * ad_rank_blocks(r));
+    ao.T = T;
+    ao.r = r;
+    ao.n = n;
+    ao.status = &hdr->status;
+    return enqueue_ad_outer(ao, s);
 }
 
 }  // extern "C"
