@@ -20,10 +20,14 @@
 // each logit is read once; sums over a token are warp reductions in float32.
 #pragma once
 #include "common.cuh"
+#include "grouped.cuh"
 
 namespace moe {
 
 constexpr int kBalWarps = 8;
+// CTAs of N values a lane that an SM holds (registers); a launch fills the
+// device once and its warps take rows in turn
+constexpr int row_ctas(int N) { return N <= 8 ? 4 : N <= 16 ? 3 : 2; }
 
 // Element i of a lane's N values of a row: vectors of VEC values, lanes side by side.
 template <int VEC>
@@ -54,6 +58,17 @@ MOE_DEVINL void load_row(const float *z, int E, int lane, float (&v)[N])
     }
 }
 
+// e^(z - m) as 2^(z log2 e - m log2 e): one fused multiply-add (whose rounding
+// of m log2 e is the same factor for the whole row and cancels in a softmax)
+// and the hardware's power of two (2^-22 relative).
+constexpr float kLog2e = 1.4426950408889634f;
+MOE_DEVINL float exp2_fast(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 MOE_DEVINL float warp_max(float v)
 {
     asm volatile("redux.sync.max.f32 %0, %0, 0xffffffff;" : "+f"(v));  // passes over NaN
@@ -82,7 +97,7 @@ struct BalanceArgs {
 };
 
 template <int VEC, int N>
-__global__ void __launch_bounds__(kBalWarps * 32) k_balance(BalanceArgs a)
+__global__ void __launch_bounds__(kBalWarps * 32, row_ctas(N)) k_balance(BalanceArgs a)
 {
     extern __shared__ uint8_t bal_smem[];
     float *sp = reinterpret_cast<float *>(bal_smem);   // [kBalWarps][E] probability sums
@@ -104,12 +119,29 @@ __global__ void __launch_bounds__(kBalWarps * 32) k_balance(BalanceArgs a)
         acc[i] = 0.0f;
     double zsum = 0.0;
     int tokens = 0;
-    for (int t = blockIdx.x * kBalWarps + warp; t < a.T; t += gridDim.x * kBalWarps) {
-        if (a.mask && !a.mask[t])
-            continue;
+    const int step = gridDim.x * kBalWarps;
+    float next[N];  // the row after this one, on its way while this one is summed
+    int next_e = MOE_EMPTY_SLOT;
+    bool next_live = false;
+    auto fetch = [&](int t) {
+        next_live = t < a.T && (!a.mask || a.mask[t]);
+        if (next_live) {
+            load_row<VEC, N>(a.logits + (size_t)t * E, E, lane, next);
+            next_e = lane < a.k1 ? a.idx[(size_t)t * a.k1 + lane] : MOE_EMPTY_SLOT;
+        }
+    };
+    int t = blockIdx.x * kBalWarps + warp;
+    fetch(t);
+    for (; t < a.T; t += step) {
         float v[N];
-        load_row<VEC, N>(a.logits + (size_t)t * E, E, lane, v);
-        const int e = lane < a.k1 ? a.idx[(size_t)t * a.k1 + lane] : MOE_EMPTY_SLOT;
+        const bool live = next_live;
+        const int e = next_e;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            v[i] = next[i];
+        fetch(t + step);
+        if (!live)
+            continue;
         float m = kNegInf;
         bool some = false;  // a row of -inf alone has no distribution and does not count
 #pragma unroll
@@ -123,7 +155,7 @@ __global__ void __launch_bounds__(kBalWarps * 32) k_balance(BalanceArgs a)
         float s = 0.0f;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            v[i] = __expf(v[i] - m);
+            v[i] = exp2_fast(fmaf(v[i], kLog2e, -m * kLog2e));
             s += v[i];
         }
         s = warp_sum(s);
@@ -264,78 +296,267 @@ MOE_DEVINL int count_from(const unsigned (&key)[N], unsigned lo)
     return __reduce_add_sync(0xffffffffu, c);
 }
 
-// The `need` largest of the warp's keys (0: not a candidate; at least `need`
-// candidates, need >= 1), equal ones by the lower row index: bit i of the
-// result marks this lane's element i.  Halves the interval of keys that holds
-// the border until a key separates exactly `need` from the rest; where equal
-// keys lie on the border, the lowest indices among them are taken one by one.
+constexpr unsigned kGivenKey = 0xffffffffu;  // above every logit's key
+
+// The key from which the warp's `want` largest keys begin (there are at least
+// `want`, 1 <= want, and fewer of kGivenKey; top: no other key is above it).
+// Halves the interval of keys that holds the border until a key separates
+// exactly `want` from the rest; where equal keys lie on the border, the lowest
+// row indices among them are raised to kGivenKey one by one.
 template <int VEC, int N>
-MOE_DEVINL unsigned select_largest(const unsigned (&key)[N], int need, int lane)
+MOE_DEVINL unsigned border_key(unsigned (&key)[N], int want, unsigned top, int lane)
 {
-    unsigned top = 0u;
+    unsigned lo = 1u, hi = top + 1u;  // at least `want` keys are >= lo, fewer are >= hi
+    if (want <= 32) {                 // 32 lanes' largest keys are all >= the least of them
+        unsigned mine = 0u;
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-        top = max(top, key[i]);
-    unsigned lo = 1u;  // at least `need` keys are >= lo, fewer are >= hi
-    if (need <= 32)    // 32 lanes' largest keys are all >= the least of them
-        lo = max(lo, __reduce_min_sync(0xffffffffu, top));
-    unsigned hi = __reduce_max_sync(0xffffffffu, top) + 1u;
-    bool exact = false;
+        for (int i = 0; i < N; ++i)
+            mine = max(mine, key[i]);
+        lo = max(lo, __reduce_min_sync(0xffffffffu, mine));
+        lo = min(lo, top);
+    }
     while (hi - lo > 1u) {
         const unsigned mid = lo + (hi - lo) / 2u;
         const int c = count_from<N>(key, mid);
-        if (c == need) {
-            lo = mid;
-            exact = true;
-            break;
-        }
-        if (c > need)
+        if (c == want)
+            return mid;
+        if (c > want)
             lo = mid;
         else
             hi = mid;
     }
-    unsigned in = 0u;
-    if (!exact && count_from<N>(key, lo) == need)
-        exact = true;
-    if (exact) {
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-            in |= (unsigned)(key[i] >= lo) << i;
-        return in;
-    }
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-        in |= (unsigned)(key[i] > lo) << i;
-    int left = need - __reduce_add_sync(0xffffffffu, __popc(in));
+    // all keys between lo and hi are lo
+    int left = want - count_from<N>(key, lo + 1u);
+    if (count_from<N>(key, lo) - want == 0)
+        return lo;
     while (left-- > 0) {
         unsigned best = 0xffffffffu;
 #pragma unroll
         for (int i = 0; i < N; ++i)
-            if (key[i] == lo && !((in >> i) & 1u))
+            if (key[i] == lo)
                 best = min(best, (unsigned)row_index<VEC>(i, lane));
         best = __reduce_min_sync(0xffffffffu, best);
 #pragma unroll
         for (int i = 0; i < N; ++i)
             if ((unsigned)row_index<VEC>(i, lane) == best)
-                in |= 1u << i;
+                key[i] = kGivenKey;
     }
-    return in;
+    return lo + 1u;
+}
+
+MOE_DEVINL float key_value(unsigned k)
+{
+    return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xffffffffu));
+}
+
+// The same border among a row's logits v themselves: true with thr where
+// exactly `want` of them (1 <= want < the row's length, largest m) are >= thr;
+// false where equal logits lie on the border.  The search first looks at each
+// lane's three largest only -- three votes a step instead of N comparisons --
+// which finds the border unless a lane holds four of the `want` largest; a
+// count over all elements says whether it did.
+template <int N>
+MOE_DEVINL bool border_value(const float (&v)[N], int want, float m, float &thr)
+{
+    const float kNegInf = -__int_as_float(0x7f800000);
+    float a = kNegInf, b = kNegInf, c = kNegInf;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const float t = fminf(a, v[i]);
+        a = fmaxf(a, v[i]);
+        const float u = fminf(b, t);
+        b = fmaxf(b, t);
+        c = fmaxf(c, u);
+    }
+    // at least `want` logits are >= lo's value, fewer are >= hi's
+    unsigned lo = order_key(kNegInf), hi = order_key(m) + 1u;
+    if (want <= 32) {  // 32 lanes' largest are all >= the least of them
+        float least = a;
+        asm volatile("redux.sync.min.f32 %0, %0, 0xffffffff;" : "+f"(least));
+        lo = min(order_key(least), hi - 1u);
+    }
+    unsigned l3 = lo, h3 = hi;
+    if (want <= 96)
+        while (h3 - l3 > 1u) {
+            const unsigned mid = l3 + (h3 - l3) / 2u;
+            const float x = key_value(mid);
+            const int n = __popc(__ballot_sync(0xffffffffu, a >= x)) +
+                          __popc(__ballot_sync(0xffffffffu, b >= x)) +
+                          __popc(__ballot_sync(0xffffffffu, c >= x));
+            if (n == want) {
+                thr = x;
+                int all = 0;
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+                    all += v[i] >= x;
+                if (__reduce_add_sync(0xffffffffu, all) == want)
+                    return true;
+                lo = mid;  // more than `want` are
+                break;
+            }
+            if (n > want)
+                l3 = mid;
+            else
+                h3 = mid;
+        }
+    while (hi - lo > 1u) {
+        const unsigned mid = lo + (hi - lo) / 2u;
+        const float x = key_value(mid);
+        int n = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            n += v[i] >= x;
+        n = __reduce_add_sync(0xffffffffu, n);
+        if (n == want) {
+            thr = x;
+            return true;
+        }
+        if (n > want)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    thr = key_value(lo);
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        n += v[i] >= thr;
+    return __reduce_add_sync(0xffffffffu, n) == want;
+}
+
+// N values of a row in shared memory (padded to whole vectors).
+template <int VEC, int N>
+MOE_DEVINL void smem_row(const float *p, int E, int lane, float (&v)[N])
+{
+#pragma unroll
+    for (int i = 0; i < N; i += VEC) {
+        const int j = row_index<VEC>(i, lane);
+        if (VEC == 4) {
+            float4 q = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (j < E)
+                q = *reinterpret_cast<const float4 *>(p + j);
+            v[i] = q.x;
+            v[i + 1] = q.y;
+            v[i + 2] = q.z;
+            v[i + 3] = q.w;
+        } else {
+            v[i] = j < E ? p[j] : 0.0f;
+        }
+    }
 }
 
 template <int VEC, int N>
-__global__ void __launch_bounds__(kBalWarps * 32) k_route_backward(RouteBackArgs a)
+MOE_DEVINL void store_row(const RouteBackArgs &a, int t, int lane, const float (&v)[N])
 {
-    extern __shared__ uint8_t rb_smem[];
+    // one rounding, to the output's type
+#pragma unroll
+    for (int i = 0; i < N; i += VEC) {
+        const int j = row_index<VEC>(i, lane);
+        if (j >= a.E)
+            continue;
+        const size_t o = (size_t)t * a.E + j;
+        if (VEC == 4) {
+            if (a.dz_bf16)
+                __stcs(reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.dz) + o),
+                       make_uint2(pack_bf16x2(v[i], v[i + 1]), pack_bf16x2(v[i + 2], v[i + 3])));
+            else
+                __stcs(reinterpret_cast<float4 *>(static_cast<float *>(a.dz) + o),
+                       make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]));
+        } else if (a.dz_bf16) {
+            static_cast<uint16_t *>(a.dz)[o] = f32_to_bf16_rn(v[i]);
+        } else {
+            static_cast<float *>(a.dz)[o] = v[i];
+        }
+    }
+}
+
+// One row whose K2 is not simply its k2 largest logits: equal logits on the
+// border, or given experts that are not among the largest.  e: the lane's
+// slot (-1: none); gw holds the slots' gradients at their experts.
+template <int VEC, int N>
+__device__ __noinline__ void route_row_general(const RouteBackArgs &a, int t, int e, float *gw,
+                                               const float *share, int lane, float m, float per,
+                                               float cb)
+{
+    const float kNegInf = -__int_as_float(0x7f800000);
+    const int E = a.E;
+    float v[N];
+    load_row<VEC, N>(a.logits + (size_t)t * E, E, lane, v);
+    unsigned key[N], thr;
+    unsigned mine = 0u;  // given elements of this lane
+    for (int s = 0; s < a.k1; ++s) {
+        const int es = __shfl_sync(0xffffffffu, e, s);
+        // row_index's inverse: the lane and element that hold expert es
+        if (es >= 0 && (es / VEC) % 32 == lane)
+            mine |= 1u << (es / (32 * VEC) * VEC + es % VEC);
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        key[i] = (mine >> i) & 1u ? kGivenKey : order_key(v[i]);
+    float m2 = m;
+    if (__reduce_add_sync(0xffffffffu, __popc(mine)) < a.k2) {
+        thr = border_key<VEC, N>(key, a.k2, order_key(m), lane);
+    } else {
+        thr = kGivenKey;
+        m2 = kNegInf;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (key[i] == kGivenKey)
+                m2 = fmaxf(m2, v[i]);
+        m2 = warp_max(m2);
+        if (m2 == kNegInf) {  // weights of 0: nothing to differentiate
+            thr = 1u;
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                key[i] = 0u;
+        }
+    }
+    const float ml = m * kLog2e, m2l = m2 * kLog2e;
+    float g[N], f[N];
+    smem_row<VEC, N>(gw, E, lane, g);
+    smem_row<VEC, N>(share, E, lane, f);
+    float s = 0.0f, fp = 0.0f, s2 = 0.0f, gs = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const float x = exp2_fast(fmaf(v[i], kLog2e, -ml));
+        const float w = key[i] >= thr ? exp2_fast(fmaf(v[i], kLog2e, -m2l)) : 0.0f;
+        s += x;
+        fp = fmaf(f[i], x, fp);
+        s2 += w;
+        if (key[i] >= thr)
+            gs = fmaf(g[i], w, gs);
+    }
+    s = warp_sum(s);
+    fp = warp_sum(fp);
+    s2 = warp_sum(s2);
+    gs = warp_sum(gs);
+    const float inv2 = s2 == 0.0f ? 0.0f : 1.0f / s2;
+    gs *= inv2;
+    const float q = per / s;
+    const float at = q * fmaf(-cb, fp / s, 2.0f * a.c_z * (m + logf(s))), qf = q * cb;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const float x = exp2_fast(fmaf(v[i], kLog2e, -ml));
+        const float w = key[i] >= thr ? exp2_fast(fmaf(v[i], kLog2e, -m2l)) : 0.0f;
+        v[i] = x * fmaf(qf, f[i], at);
+        if (key[i] >= thr)
+            v[i] = fmaf(w, inv2 * (g[i] - gs), v[i]);
+    }
+    store_row<VEC, N>(a, t, lane, v);
+}
+
+template <int VEC, int N>
+__global__ void __launch_bounds__(kBalWarps * 32, row_ctas(N)) k_route_backward(RouteBackArgs a)
+{
+    extern __shared__ __align__(16) uint8_t rb_smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int E = a.E, Ep = (E + 3) & ~3;
-    float *share = reinterpret_cast<float *>(rb_smem);         // [Ep] f_e
-    float *gw = share + Ep + warp * Ep;                        // [Ep] of this warp: dL/dw, zero
-    uint32_t *given = reinterpret_cast<uint32_t *>(share + (kBalWarps + 1) * Ep) + warp * 32;
+    float *share = reinterpret_cast<float *>(rb_smem);  // [Ep] f_e
+    float *gw = share + Ep + warp * Ep;                 // [Ep] of this warp: dL/dw, zero between rows
     __shared__ int total;
     const float kNegInf = -__int_as_float(0x7f800000);
     for (int e = tid; e < (kBalWarps + 1) * Ep; e += kBalWarps * 32)
         share[e] = 0.0f;
-    given[lane] = 0u;
     if (tid == 0)
         total = 0;
     __syncthreads();
@@ -356,152 +577,118 @@ __global__ void __launch_bounds__(kBalWarps * 32) k_route_backward(RouteBackArgs
         per = (a.d_loss ? __ldg(a.d_loss) : 1.0f) / (float)max(__ldg(&a.counts[E]), 1);
         __syncthreads();
     }
+    const float cb = a.c_bal * (float)E;
 
     for (int t = blockIdx.x * kBalWarps + warp; t < a.T; t += gridDim.x * kBalWarps) {
-        float v[N];
-        bool some = false;
-        if (!a.mask || a.mask[t]) {
+        float v[N];  // the logits, then the gradient
+        float m = kNegInf;
+        bool live = !a.mask || a.mask[t];
+        int e = MOE_EMPTY_SLOT;
+        float ge = 0.0f, ze = kNegInf;  // the lane's slot: expert, gradient, logit
+        if (live) {
+            if (a.d_w && lane < a.k1) {
+                e = a.idx[(size_t)t * a.k1 + lane];
+                ge = a.d_w[(size_t)t * a.k1 + lane];
+            }
             load_row<VEC, N>(a.logits + (size_t)t * E, E, lane, v);
-#pragma unroll
-            for (int i = 0; i < N; ++i)
-                some |= !(v[i] == kNegInf);
-        }
-        float dz[N];
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-            dz[i] = 0.0f;
-        if (__any_sync(0xffffffffu, some)) {
-            float m = kNegInf;
+            if ((unsigned)e >= (unsigned)E) {
+                if (e != MOE_EMPTY_SLOT)
+                    set_status(a.status, MOE_ERR_DEVICE_CHECK);
+                e = -1;
+                ge = 0.0f;
+            } else {
+                ze = __ldcg(a.logits + (size_t)t * E + e);
+            }
 #pragma unroll
             for (int i = 0; i < N; ++i)
                 m = fmaxf(m, v[i]);
             m = warp_max(m);
-            if (a.d_w) {
-                // the given slots: their gradients (summed in slot order) and a bit each
-                int e = lane < a.k1 ? a.idx[(size_t)t * a.k1 + lane] : MOE_EMPTY_SLOT;
-                const float g = lane < a.k1 ? a.d_w[(size_t)t * a.k1 + lane] : 0.0f;
-                if ((unsigned)e >= (unsigned)E) {
-                    if (e != MOE_EMPTY_SLOT)
-                        set_status(a.status, MOE_ERR_DEVICE_CHECK);
-                    e = -1;
-                }
+            if (m == kNegInf) {  // -inf alone (no distribution) or NaN among it
+                bool nan = false;
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+                    nan |= v[i] != v[i];
+                live = __any_sync(0xffffffffu, nan);
+            }
+        }
+        if (!live) {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                v[i] = 0.0f;
+            store_row<VEC, N>(a, t, lane, v);
+            continue;
+        }
+        // K2 as "z >= thr"; the general row where that is not it
+        float thr = -kNegInf;
+        bool simple = true;
+        if (a.d_w) {
+            // the slots' gradients by expert; repeated experts add in slot order
+            const unsigned same = __match_any_sync(0xffffffffu, e);
+            const bool again = e >= 0 && (same & ((1u << lane) - 1u));  // not its expert's first
+            if (e >= 0 && !again)
+                gw[e] = ge;
+            __syncwarp();
+            if (__any_sync(0xffffffffu, again))
                 for (int s = 0; s < a.k1; ++s) {
-                    if (lane == s && e >= 0) {
-                        gw[e] += g;
-                        given[e >> 5] |= 1u << (e & 31);
-                    }
+                    if (lane == s && again)
+                        gw[e] += ge;
                     __syncwarp();
                 }
-                float gv[N];
-                unsigned set = 0u;
-#pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    const int j = row_index<VEC>(i, lane);
-                    gv[i] = 0.0f;
-                    if (j < E) {
-                        gv[i] = gw[j];
-                        set |= ((given[j >> 5] >> (j & 31)) & 1u) << i;
-                    }
-                }
-                __syncwarp();
-                if (e >= 0) {
-                    gw[e] = 0.0f;
-                    given[e >> 5] = 0u;
-                }
-                __syncwarp();
-                if (a.k2 >= E) {
-                    set = 0xffffffffu;
-                } else {
-                    const int need = a.k2 - __reduce_add_sync(0xffffffffu, __popc(set));
-                    if (need > 0) {
-                        unsigned key[N];
-#pragma unroll
-                        for (int i = 0; i < N; ++i)
-                            key[i] = row_index<VEC>(i, lane) < E && !((set >> i) & 1u)
-                                         ? order_key(v[i])
-                                         : 0u;
-                        set |= select_largest<VEC, N>(key, need, lane);
-                    }
-                }
-                // softmax over the set and its gradient
-                float m2 = kNegInf;
-                bool in_set = false;
-#pragma unroll
-                for (int i = 0; i < N; ++i)
-                    if ((set >> i) & 1u) {
-                        m2 = fmaxf(m2, v[i]);
-                        in_set |= !(v[i] == kNegInf);
-                    }
-                m2 = warp_max(m2);
-                if (__any_sync(0xffffffffu, in_set)) {
-                    float s2 = 0.0f, gs = 0.0f;
-#pragma unroll
-                    for (int i = 0; i < N; ++i) {
-                        dz[i] = (set >> i) & 1u ? __expf(v[i] - m2) : 0.0f;
-                        s2 += dz[i];
-                        gs = fmaf(gv[i], dz[i], gs);
-                    }
-                    s2 = warp_sum(s2);
-                    gs = warp_sum(gs) / s2;
-                    const float inv = 1.0f / s2;
-#pragma unroll
-                    for (int i = 0; i < N; ++i)
-                        dz[i] = (set >> i) & 1u ? dz[i] * inv * (gv[i] - gs) : 0.0f;
-                }
-            }
-            if (a.counts) {
-                float s = 0.0f, fp = 0.0f;
-                float f[N];
-#pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    const int j = row_index<VEC>(i, lane);
-                    f[i] = j < E ? share[j] : 0.0f;
-                    v[i] = __expf(v[i] - m);
-                    s += v[i];
-                    fp = fmaf(f[i], v[i], fp);
-                }
-                s = warp_sum(s);
-                fp = warp_sum(fp);
-                const float inv = 1.0f / s;
-                const float lse = m + logf(s);
-                const float cb = a.c_bal * (float)E;
-                const float at = fmaf(-cb, fp * inv, 2.0f * a.c_z * lse);
-#pragma unroll
-                for (int i = 0; i < N; ++i)
-                    dz[i] = fmaf(per * (v[i] * inv), fmaf(cb, f[i], at), dz[i]);
-            }
+            simple = a.k2 >= E || border_value<N>(v, a.k2, m, thr);
+            if (a.k2 >= E)
+                thr = kNegInf;
+            simple = simple && !__any_sync(0xffffffffu, e >= 0 && !(ze >= thr));
         }
-        // one rounding, to the output's type
+        if (!simple) {
+            route_row_general<VEC, N>(a, t, e, gw, share, lane, m, per, cb);
+        } else {
+            // dz = e^(z - m) (1/S2 (g - sum g w) in K2  +  per/S (cb (f - sum f p) + 2 c_z lse))
+            const float ml = m * kLog2e;
+            float s = 0.0f, fp = 0.0f, s2 = 0.0f;
+            float gs = ge * (e >= 0 ? exp2_fast(fmaf(ze, kLog2e, -ml)) : 0.0f);
+            float f[N];
+            smem_row<VEC, N>(share, E, lane, f);
 #pragma unroll
-        for (int i = 0; i < N; i += VEC) {
-            const int j = row_index<VEC>(i, lane);
-            if (j >= E)
-                continue;
-            const size_t o = (size_t)t * E + j;
-            if (VEC == 4) {
-                if (a.dz_bf16) {
-                    const uint32_t lo = (uint32_t)f32_to_bf16_rn(dz[i]) |
-                                        ((uint32_t)f32_to_bf16_rn(dz[i + 1]) << 16);
-                    const uint32_t hi = (uint32_t)f32_to_bf16_rn(dz[i + 2]) |
-                                        ((uint32_t)f32_to_bf16_rn(dz[i + 3]) << 16);
-                    __stcs(reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.dz) + o),
-                           make_uint2(lo, hi));
-                } else {
-                    __stcs(reinterpret_cast<float4 *>(static_cast<float *>(a.dz) + o),
-                           make_float4(dz[i], dz[i + 1], dz[i + 2], dz[i + 3]));
-                }
-            } else if (a.dz_bf16) {
-                static_cast<uint16_t *>(a.dz)[o] = f32_to_bf16_rn(dz[i]);
-            } else {
-                static_cast<float *>(a.dz)[o] = dz[i];
+            for (int i = 0; i < N; ++i) {
+                const float x = exp2_fast(fmaf(v[i], kLog2e, -ml));
+                s += x;
+                fp = fmaf(f[i], x, fp);
+                if (v[i] >= thr)
+                    s2 += x;
             }
+#pragma unroll
+            for (int o = 16; o >= 1; o >>= 1) {
+                s += __shfl_xor_sync(0xffffffffu, s, o);
+                fp += __shfl_xor_sync(0xffffffffu, fp, o);
+                s2 += __shfl_xor_sync(0xffffffffu, s2, o);
+                gs += __shfl_xor_sync(0xffffffffu, gs, o);
+            }
+            const float inv2 = s2 == 0.0f ? 0.0f : 1.0f / s2;  // 0: no weights asked for
+            gs *= inv2 * inv2;
+            const float inv = 1.0f / s, q = per * inv;
+            const float at = q * fmaf(-cb, fp * inv, 2.0f * a.c_z * (m + logf(s))), qf = q * cb;
+            float g[N];
+            smem_row<VEC, N>(gw, E, lane, g);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const float x = exp2_fast(fmaf(v[i], kLog2e, -ml));
+                float k = fmaf(qf, f[i], at);
+                if (v[i] >= thr)
+                    k += fmaf(g[i], inv2, -gs);
+                v[i] = x * k;
+            }
+            store_row<VEC, N>(a, t, lane, v);
         }
+        __syncwarp();
+        if (e >= 0)
+            gw[e] = 0.0f;
+        __syncwarp();
     }
 }
 
 inline size_t route_backward_smem_bytes(int E)
 {
-    return sizeof(float) * (kBalWarps + 1) * ((E + 3) & ~3) + sizeof(uint32_t) * 32 * kBalWarps;
+    return sizeof(float) * (kBalWarps + 1) * ((E + 3) & ~3);
 }
 
 }  // namespace moe

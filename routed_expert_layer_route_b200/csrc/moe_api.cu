@@ -1869,17 +1869,17 @@ static int bal_check(int T, int E, int k1)
         CALL(1, 32);                          \
     } while (0)
 
-static int row_grid(int T)
+static int row_grid(int T, int N)
 {
-    const int g = (T + kBalWarps - 1) / kBalWarps;
-    return g < kBalMaxGrid ? g : kBalMaxGrid;
+    const int g = (T + kBalWarps - 1) / kBalWarps, most = 148 * row_ctas(N);
+    return g < most ? g : most;
 }
 
 static int enqueue_balance(const BalanceArgs &a, cudaStream_t s)
 {
     const int E = a.E;
 #define MOE_BAL(VEC, N)                                                                        \
-    return launch(k_balance<VEC, N>, dim3(row_grid(a.T)), dim3(kBalWarps * 32),                \
+    return launch(k_balance<VEC, N>, dim3(row_grid(a.T, N)), dim3(kBalWarps * 32),                \
                   balance_smem_bytes(E), s, kPdl, a)
     MOE_ROW_VARIANTS(MOE_BAL);
 #undef MOE_BAL
@@ -1889,7 +1889,7 @@ static int enqueue_route_backward(const RouteBackArgs &a, cudaStream_t s)
 {
     const int E = a.E;
 #define MOE_RB(VEC, N)                                                                         \
-    return launch(k_route_backward<VEC, N>, dim3(row_grid(a.T)), dim3(kBalWarps * 32),         \
+    return launch(k_route_backward<VEC, N>, dim3(row_grid(a.T, N)), dim3(kBalWarps * 32),         \
                   route_backward_smem_bytes(E), s, kPdl, a)
     MOE_ROW_VARIANTS(MOE_RB);
 #undef MOE_RB
