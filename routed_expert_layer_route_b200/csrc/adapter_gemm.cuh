@@ -8,11 +8,10 @@
 // it lands in the same tensor-memory accumulator before the one store of y.
 // A tile of 256 rows takes only the adapters that occur in it.  Its U operand
 // is written by four warps of each CTA -- a row's own adapter's u, zeros for
-// the others -- in the two bf16 parts (hi, lo: u to 16 bits), its B operand
-// is a TMA copy of B_a as it lies in memory (16 ranks x outputs, the operand
-// whose rows run along N).  Each unit of 16 ranks costs two matrix
-// instructions where din costs din / 16, so one adapter of rank 16 in a tile
-// adds 2 to din / 16 instructions.
+// the others -- in its three bf16 parts, its B operand is a TMA copy of B_a as
+// it lies in memory (16 ranks x outputs, the operand whose rows run along N).
+// Each unit of 16 ranks costs three matrix instructions where din costs
+// din / 16, so one adapter of rank 16 in a tile adds 3 to din / 16.
 //
 // Zeros do not silence a NaN or inf: 0 x inf is NaN, so a broken adapter
 // would reach the other rows of its tile.  Every such product is a NaN, so
@@ -41,7 +40,7 @@ constexpr int kAGRows = 256;    // rows of a pair's tile
 constexpr int kAGThreads = 448;
 constexpr int kAGWarpU = 10;    // first of the U warps
 constexpr int kAGEpiWarps = 8;
-constexpr int kAGUBufs = 2;     // U/B buffers, two units of 16 ranks each
+constexpr int kAGUBufs = 3;     // U/B buffers, a unit of 16 ranks each
 constexpr int kAGTileA = 128 * kGBK * 2;  // 16 KB: a CTA's rows of one K block
 
 template <int BN>
@@ -50,7 +49,7 @@ struct AGShape {
     static constexpr int kStage = kAGTileA + kTileB;
     static constexpr int kStages = BN == 256 ? 5 : 6;
     static constexpr int kUnitB = BN / 2 * 16 * 2;       // a CTA's outputs of one unit
-    static constexpr int kUBuf = kAGTileA + 2 * kUnitB;
+    static constexpr int kUBuf = kAGTileA + kUnitB;
 };
 
 struct AGSync {
@@ -62,7 +61,7 @@ struct AGSync {
     uint64_t acc_empty[2];        // CTA 0: both epilogues have read set b
     uint64_t drained;             // each CTA: every MMA has completed
     uint64_t bye;                 // each CTA: the other CTA has finished
-    int u_units[kAGUBufs];        // units in the buffer, + 4: the tile's last buffer
+    int u_what[kAGUBufs];         // 1: a unit is in the buffer, + 2: the tile's last buffer
     uint32_t tmem_base;
     int abort;
     uint32_t bits[32];            // the adapters of a tile
@@ -233,18 +232,19 @@ __global__ void __launch_bounds__(kAGThreads, 1)
                         break;
                     }
                     tc_fence_after();
-                    const int units = *(volatile int *)&sy.u_units[b];
+                    const int what = *(volatile int *)&sy.u_what[b];
                     const uint32_t st = smem_addr(ubuf + (size_t)b * S::kUBuf);
-                    for (int k = 0; k < (units & 3); ++k) {
-                        const uint64_t bd =
-                            umma_desc_mn_sw128(st + kAGTileA + k * S::kUnitB, 2048);
-                        umma_bf16_pair(dt, umma_desc_sw128(st + k * 64), bd, idesc_mn, acc);
-                        umma_bf16_pair(dt, umma_desc_sw128(st + k * 64 + 32), bd, idesc_mn, 1);
-                        acc = 1;
+                    if (what & 1) {
+                        const uint64_t bd = umma_desc_mn_sw128(st + kAGTileA, 2048);
+#pragma unroll
+                        for (int k = 0; k < kAdParts; ++k) {
+                            umma_bf16_pair(dt, umma_desc_sw128(st + k * 32), bd, idesc_mn, acc);
+                            acc = 1;
+                        }
                     }
                     umma_commit_pair_both(&sy.uempty[b]);
                     ++ub;
-                    if (units & 4)
+                    if (what & 2)
                         break;
                 }
                 if (ag_aborted(sy))
@@ -259,7 +259,6 @@ __global__ void __launch_bounds__(kAGThreads, 1)
         const int ut = tid - kAGWarpU * 32;  // this CTA's row of the tile
         const int rp = ad_rp(p.r);
         uint32_t ub = 0;
-        pdl_wait();
         for (int i = pair; i < tiles; i += pairs) {
             // the tile's adapters, both CTAs' rows, in order of their number
             const int tb = i / ncol * kAGRows;
@@ -301,10 +300,22 @@ __global__ void __launch_bounds__(kAGThreads, 1)
             named_bar_sync(1, 128);
             const int units = sy.count * nch;
             const int o0 = i % ncol * BN + (int)rank * (BN / 2);
-            const uint16_t *urow = p.parts + (size_t)(a >= 0 ? t : 0) * 2 * rp;
+            const uint16_t *urow = p.parts + (size_t)(a >= 0 ? t : 0) * kAdParts * rp;
+            // this row's next unit of u, loaded before its turn comes
+            uint4 own[2 * kAdParts] = {};
+            auto load_own = [&](int j) {
+#pragma unroll
+                for (int c = 0; c < 2 * kAdParts; ++c)
+                    own[c] = __ldcg(reinterpret_cast<const uint4 *>(urow + c / 2 * rp + j) + c % 2);
+            };
+            if (i == pair)
+                pdl_wait();
+            if (a >= 0)
+                load_own(0);
             int u0 = 0;
             do {
-                const int b = ub % kAGUBufs, nu = min(2, units - u0);
+                const int b = ub % kAGUBufs;
+                const int e = u0 < units ? sy.list[u0 / nch] : -1, j = u0 % nch * 16;
                 // one lane waits for its warp
                 int ok = 1;
                 if (lane == 0)
@@ -316,39 +327,27 @@ __global__ void __launch_bounds__(kAGThreads, 1)
                 uint8_t *st = ubuf + (size_t)b * S::kUBuf;
                 if (ut == 0) {
                     if (lead)
-                        sy.u_units[b] = nu | (u0 + 2 >= units ? 4 : 0);
+                        sy.u_what[b] = (e >= 0 ? 1 : 0) | (u0 + 1 >= units ? 2 : 0);
                     const uint32_t fb = cluster_addr(&sy.ufull[b], 0);
-                    if (lead && nu > 0)
-                        mbar_expect_tx(&sy.ufull[b], 2 * nu * S::kUnitB);
-                    for (int k = 0; k < nu; ++k) {
-                        const int e = sy.list[(u0 + k) / nch], j = (u0 + k) % nch * 16;
+                    if (e >= 0) {
+                        if (lead)
+                            mbar_expect_tx(&sy.ufull[b], 2 * S::kUnitB);
                         for (int c = 0; c < BN / 128; ++c)
-                            tma_load_3d_pair(st + kAGTileA + k * S::kUnitB + c * 2048, &tm_b,
-                                             o0 + 64 * c, j, e, fb);
+                            tma_load_3d_pair(st + kAGTileA + c * 2048, &tm_b, o0 + 64 * c, j, e, fb);
                     }
                 }
-                for (int k = 0; k < nu; ++k) {
-                    const int e = sy.list[(u0 + k) / nch], j = (u0 + k) % nch * 16;
-                    uint4 v[4] = {};
-                    if (a == e) {
-                        const uint4 *h = reinterpret_cast<const uint4 *>(urow + j);
-                        const uint4 *l = reinterpret_cast<const uint4 *>(urow + rp + j);
-                        v[0] = __ldcg(h);
-                        v[1] = __ldcg(h + 1);
-                        v[2] = __ldcg(l);
-                        v[3] = __ldcg(l + 1);
-                    }
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        *reinterpret_cast<uint4 *>(st + ut * 128 +
-                                                   (((k * 4 + c) ^ (ut & 7)) << 4)) = v[c];
-                }
+                for (int c = 0; c < 2 * kAdParts; ++c)
+                    *reinterpret_cast<uint4 *>(st + ut * 128 + ((c ^ (ut & 7)) << 4)) =
+                        a >= 0 && a == e ? own[c] : make_uint4(0u, 0u, 0u, 0u);
+                if (a >= 0 && a == e && j + 16 < rp)
+                    load_own(j + 16);
                 asm volatile("fence.proxy.async;" ::: "memory");
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive_cluster(cluster_addr(&sy.ufull[b], 0));
                 ++ub;
-                u0 += 2;
+                ++u0;
             } while (u0 < units);
             named_bar_sync(1, 128);  // the list has been read; all four warps see an abort
             if (ag_aborted(sy))
@@ -372,7 +371,6 @@ __global__ void __launch_bounds__(kAGThreads, 1)
                 break;
             }
             tc_fence_after();
-            const int a = t < p.T ? adapter_of(p.adapter, t, p.n, nullptr) : -1;
 #pragma unroll 1
             for (int c = eh; c < BN / 32; c += 2) {
                 const int o = o0 + c * 32;
@@ -387,11 +385,13 @@ __global__ void __launch_bounds__(kAGThreads, 1)
 #pragma unroll
                 for (int j = 0; j < 32; ++j)
                     bad |= v[j] != v[j];
-                if (bad)
+                if (bad) {
+                    const int a = adapter_of(p.adapter, t, p.n, nullptr);
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
                         if (v[j] != v[j] && o + j < p.dout)
                             v[j] = ag_one(p, a, t, o + j);
+                }
                 const size_t at = (size_t)t * p.dout + o;
                 // dout % 8 == 0: vectors of eight outputs are whole or absent
 #pragma unroll

@@ -182,6 +182,17 @@ static int device_info(DevInfo *&out)
             return MOE_ERR_CUDA;
         if (cudaFuncSetAttribute(k_ad_gemm<256>, dsm, (int)ag_smem_bytes<256>()) != cudaSuccess ||
             cudaFuncSetAttribute(k_ad_gemm<128>, dsm, (int)ag_smem_bytes<128>()) != cudaSuccess ||
+            cudaFuncSetAttribute(k_ad_rows<1, false>, dsm, AdRowsShape<1>::kBytes) != cudaSuccess ||
+            cudaFuncSetAttribute(k_ad_rows<2, false>, dsm, AdRowsShape<2>::kBytes) != cudaSuccess ||
+            cudaFuncSetAttribute(k_ad_rows<4, false>, dsm, AdRowsShape<4>::kBytes) != cudaSuccess ||
+            cudaFuncSetAttribute(k_ad_rows<8, false>, dsm, AdRowsShape<8>::kBytes) != cudaSuccess ||
+            cudaFuncSetAttribute(k_ad_rows<1, true>, dsm, AdRowsShape<1>::kBytes) != cudaSuccess ||
+            cudaFuncSetAttribute(k_ad_rows<2, true>, dsm, AdRowsShape<2>::kBytes) != cudaSuccess ||
+            cudaFuncSetAttribute(k_ad_rows<4, true>, dsm, AdRowsShape<4>::kBytes) != cudaSuccess ||
+            cudaFuncSetAttribute(k_ad_rows<8, true>, dsm, AdRowsShape<8>::kBytes) != cudaSuccess ||
+            cudaFuncSetAttribute(k_ad_inner_big<2>, dsm, AdBigShape<2>::kBytes) != cudaSuccess ||
+            cudaFuncSetAttribute(k_ad_inner_big<4>, dsm, AdBigShape<4>::kBytes) != cudaSuccess ||
+            cudaFuncSetAttribute(k_ad_inner_big<8>, dsm, AdBigShape<8>::kBytes) != cudaSuccess ||
             cudaFuncSetAttribute(k_ad_outer<1>, dsm, AdOuterSmem<1>::kBytes) != cudaSuccess ||
             cudaFuncSetAttribute(k_ad_outer<2>, dsm, AdOuterSmem<2>::kBytes) != cudaSuccess ||
             cudaFuncSetAttribute(k_ad_outer<4>, dsm, AdOuterSmem<4>::kBytes) != cudaSuccess)
@@ -1514,7 +1525,7 @@ extern "C" int moe_noalloc_read_status(int *status_out, void *stream)
 // ========================================================================== adapters
 namespace moe {
 
-constexpr int kAdMaxDim = 16384, kAdMaxR = 128, kAdMaxN = 1024;
+constexpr int kAdMaxDim = 16384, kAdMaxN = 1024;
 
 struct AdLayout {
     size_t parts, given, offsets, row, pos, hist, arrive, partial, total;
@@ -1543,8 +1554,8 @@ static AdLayout ad_layout(int T, int din, int dout, int r, int n)
     size_t o = sizeof(WsHeader);
     const size_t rows = (size_t)T;
     const size_t rp = (size_t)((r + 15) & ~15), both = (size_t)r * (din + dout);
-    L.parts = o;    o = align256(o + 4 * rows * rp);
-    L.given = o;    o = align256(o + 4 * rows * rp);
+    L.parts = o;    o = align256(o + sizeof(uint16_t) * kAdParts * rows * rp);
+    L.given = o;    o = align256(o + sizeof(uint16_t) * kAdParts * rows * rp);
     L.offsets = o;  o = align256(o + sizeof(int32_t) * (size_t)(n + 1));
     L.row = o;      o = align256(o + sizeof(int32_t) * rows);
     L.pos = o;      o = align256(o + sizeof(int32_t) * rows);
@@ -1580,30 +1591,50 @@ static int ad_check_ws(const void *ws, size_t ws_bytes, size_t need)
     return ws_bytes < need ? MOE_ERR_WORKSPACE_TOO_SMALL : MOE_OK;
 }
 
+// From here on 64-row tiles (k_ad_inner_big) use the device better than 16-row
+// ones split over K.
+constexpr int kAdBigRows = 2048;
+
 // Inner products (and, with conv or zero_n, CTAs behind them for those).
 static int enqueue_ad_inner(AdInnerArgs a, bool inner, cudaStream_t s)
 {
-    const int tiles = (a.T + kAdTile - 1) / kAdTile;
-    // CTAs that share a tile's adapters: 16 where the tiles alone leave the
-    // device empty, fewer as they fill it
-    int lists = 2 * 148 / tiles;
-    a.lists = lists < 1 ? 1 : lists > kAdTile ? kAdTile : lists;
-    a.inner_ctas = inner ? tiles * a.lists : 0;
     const int rp = (a.r + 15) & ~15;
     const int64_t vals = a.conv ? (int64_t)a.T * rp : a.zero_n;
     int64_t extra = (vals + 2047) / 2048;
+    if (a.row && a.u_out && extra < 16)
+        extra = 16;
     if (extra > 148)
         extra = 148;
+    const dim3 block(kAdWarps * 32), big(kAdBigWarps * 32);
+    if (inner && a.T >= kAdBigRows) {
+        a.lists = 2;  // a tile in which two requests meet takes no longer than the others
+        a.inner_ctas = (a.T + 63) / 64 * a.lists;
+        const unsigned gx = (unsigned)(a.inner_ctas + extra);
+        if (rp <= 16)
+            return launch(k_ad_inner_big<2>, dim3(gx, 1), big, AdBigShape<2>::kBytes, s, kPdl, a);
+        if (rp <= 32)
+            return launch(k_ad_inner_big<4>, dim3(gx, 1), big, AdBigShape<4>::kBytes, s, kPdl, a);
+        return launch(k_ad_inner_big<8>, dim3(gx, (rp + 63) / 64), big, AdBigShape<8>::kBytes, s,
+                      kPdl, a);
+    }
+    const int tiles = (a.T + 15) / 16;
+    // CTAs that share a tile's adapters: 16 where the tiles alone leave the
+    // device empty, fewer as they fill it
+    int lists = 2 * 148 / tiles;
+    a.lists = lists < 1 ? 1 : lists > 16 ? 16 : lists;
+    a.inner_ctas = inner ? tiles * a.lists : 0;
     if (a.inner_ctas + extra == 0)
         return MOE_OK;
     const unsigned gx = (unsigned)(a.inner_ctas + extra);
-    const dim3 block(kAdWarps * 32);
+#define MOE_AD_INNER(NT) \
+    return launch(k_ad_inner<1, NT>, dim3(gx, (rp + 8 * NT - 1) / (8 * NT)), block, 0, s, kPdl, a)
     // ranks of a CTA: 16 while the rows are few and CTAs would idle, else up to 64
     if (rp <= 16 || a.T <= kAdRows)
-        return launch(k_ad_inner<2>, dim3(gx, (rp + 15) / 16), block, 0, s, kPdl, a);
+        MOE_AD_INNER(2);
     if (rp <= 32)
-        return launch(k_ad_inner<4>, dim3(gx, 1), block, 0, s, kPdl, a);
-    return launch(k_ad_inner<8>, dim3(gx, (rp + 63) / 64), block, 0, s, kPdl, a);
+        MOE_AD_INNER(4);
+    MOE_AD_INNER(8);
+#undef MOE_AD_INNER
 }
 
 // [n x r x cols] bf16 read in boxes of 64 columns x 16 ranks, zeros behind r.
@@ -1623,17 +1654,34 @@ static int rank_tile_map(CUtensorMap *m, const void *base, uint64_t cols, uint64
     return rc == CUDA_SUCCESS ? MOE_OK : MOE_ERR_CUDA;
 }
 
-static int enqueue_ad_product(AdProductArgs a, cudaStream_t s)
+// one: the inner step's inputs where this launch does that step too
+static int enqueue_ad_product(AdProductArgs a, cudaStream_t s, const AdOne *one = nullptr)
 {
     if (a.T <= kAdRows) {
         const dim3 block(kAdWarps * 32), grid((a.dout + 15) / 16);
+        DevInfo *di;
+        const int rc = device_info(di);
+        if (rc != MOE_OK)
+            return rc;
+        const AdOne o = one ? *one : AdOne{};
+#define MOE_AD_ROWS(NT, ONE) \
+    return launch(k_ad_rows<NT, ONE>, grid, block, AdRowsShape<NT>::kBytes, s, kPdl, a, o)
+        if (one && a.T <= 8)
+            MOE_AD_ROWS(1, true);
+        if (one && a.T <= 16)
+            MOE_AD_ROWS(2, true);
+        if (one && a.T <= 32)
+            MOE_AD_ROWS(4, true);
+        if (one)
+            MOE_AD_ROWS(8, true);
         if (a.T <= 8)
-            return launch(k_ad_rows<1>, grid, block, 0, s, kPdl, a);
+            MOE_AD_ROWS(1, false);
         if (a.T <= 16)
-            return launch(k_ad_rows<2>, grid, block, 0, s, kPdl, a);
+            MOE_AD_ROWS(2, false);
         if (a.T <= 32)
-            return launch(k_ad_rows<4>, grid, block, 0, s, kPdl, a);
-        return launch(k_ad_rows<8>, grid, block, 0, s, kPdl, a);
+            MOE_AD_ROWS(4, false);
+        MOE_AD_ROWS(8, false);
+#undef MOE_AD_ROWS
     }
     DevInfo *di;
     int rc;
@@ -1658,6 +1706,27 @@ static int enqueue_ad_product(AdProductArgs a, cudaStream_t s)
                       kPdl | kPair, tx, tw, tb, a);
     return launch(k_ad_gemm<128>, grid, dim3(kAGThreads), ag_smem_bytes<128>(), s, kPdl | kPair, tx,
                   tw, tb, a);
+}
+
+// Rows grouped by adapter (offsets, row): one CTA, or for large batches the
+// counting sort of the routed slots with one slot a row.
+static int enqueue_ad_group(const int32_t *adapter, int T, int n, void *ws, const AdLayout &L,
+                            cudaStream_t s)
+{
+    int32_t *offsets = at<int32_t>(ws, L.offsets), *row = at<int32_t>(ws, L.row);
+    int *status = &static_cast<WsHeader *>(ws)->status;
+    if (T <= kAdGroupMaxT && n <= kAdGroupMaxN)
+        return launch(k_ad_group, dim3(1), dim3(kAdGroupWarps * 32), ad_group_smem_bytes(n), s, kPdl,
+                      adapter, T, n, offsets, row, status);
+    const PermOut po = {offsets, row, at<int32_t>(ws, L.pos), nullptr, nullptr};
+    return enqueue_perm_parallel(adapter, T, 1, n, at<int>(ws, L.hist), po, status, s);
+}
+
+// The product's CTAs compute u themselves: a few row-ranks, and not so many
+// CTAs that reading the adapters in each costs more than the inner launch.
+static bool ad_one_launch(int T, int dout, int r)
+{
+    return T * r <= kAdOneRanks && (int64_t)T * r * dout <= 64 * 1024;
 }
 
 static int enqueue_ad_outer(AdOuterArgs a, cudaStream_t s)
@@ -1719,11 +1788,21 @@ int moe_adapter_linear(const void *x_bf16, const void *w_bf16, const float *bias
     ai.r = r;
     ai.n = n;
     ai.status = &hdr->status;
-    if ((rc = enqueue_ad_inner(ai, true, s)) != MOE_OK)
-        return rc;
     AdProductArgs ap = {x, static_cast<const uint16_t *>(w_bf16), bias,
                         static_cast<const uint16_t *>(lora_b_bf16), adapter, ai.parts, y,
                         y_dtype == MOE_DTYPE_BF16, T, din, dout, r, n, hdr};
+    if (ad_one_launch(T, dout, r)) {
+        const AdOne one = {ai.a, scale, u_out};
+        return enqueue_ad_product(ap, s, &one);
+    }
+    if (T >= kAdBigRows && n > 1) {  // tiles of few adapters, however the rows come
+        if ((rc = enqueue_ad_group(adapter, T, n, ws, L, s)) != MOE_OK)
+            return rc;
+        ai.row = at<int32_t>(ws, L.row);
+        ai.rows = at<int32_t>(ws, L.offsets) + n;
+    }
+    if ((rc = enqueue_ad_inner(ai, true, s)) != MOE_OK)
+        return rc;
     return enqueue_ad_product(ap, s);
 }
 
@@ -1767,12 +1846,7 @@ int moe_adapter_backward(const void *dy_bf16, const void *x_bf16, const void *w_
     int32_t *offsets = at<int32_t>(ws, L.offsets), *row = at<int32_t>(ws, L.row);
     const bool outer = d_lora_a || d_lora_b;
     if (outer) {
-        // rows grouped by adapter: the counting sort of the routed slots, one slot a row
-        PermOut po = {offsets, row, at<int32_t>(ws, L.pos), nullptr, nullptr};
-        rc = T > 4096 ? enqueue_perm_parallel(adapter, T, 1, n, at<int>(ws, L.hist), po,
-                                              &hdr->status, s)
-                      : launch(k_permute, dim3(1), dim3(1024), permute_smem_bytes(n, T), s, kPdl,
-                               adapter, T, 1, n, po, &hdr->status);
+        rc = enqueue_ad_group(adapter, T, n, ws, L, s);
         if (rc != MOE_OK)
             return rc;
     }
@@ -1792,6 +1866,10 @@ int moe_adapter_backward(const void *dy_bf16, const void *x_bf16, const void *w_
     ai.r = r;
     ai.n = n;
     ai.status = &hdr->status;
+    if (outer) {  // the grouping is there: a tile then has few adapters, however the rows come
+        ai.row = row;
+        ai.rows = offsets + n;
+    }
     if ((rc = enqueue_ad_inner(ai, dx || d_lora_a, s)) != MOE_OK)
         return rc;
     if (dx) {
