@@ -120,8 +120,7 @@ struct AdInnerArgs {
     const float *conv;       // nullable [T x r]: given u to split into conv_parts
     uint16_t *conv_parts;    // [T][kAdParts][rp]
     int T, din, r, n;
-    int *zero;               // nullable: zero_n counters to clear for the outer step
-    int zero_n;
+    int zero_u;              // clear u_out in rows without an adapter (k_ad_inner_big)
     int lists;               // CTAs that share a row tile's adapters
     int inner_ctas;          // CTAs of the inner products; those behind them convert
     int *status;
@@ -138,83 +137,108 @@ MOE_DEVINL void ad_put_parts(uint16_t *parts, int rp, int t, int j, float v)
         parts[((size_t)t * kAdParts + i) * rp + j] = q[i];
 }
 
-// The CTAs behind the inner products: the given u into its parts, and the
-// outer step's counters to zero.
+// The CTAs behind the inner products: the given u into its parts, and zeros
+// for rows without an adapter.
 MOE_DEVINL void ad_convert(const AdInnerArgs &p, int tid)
 {
     const int rp = ad_rp(p.r);
-    const int64_t all = (int64_t)p.T * rp;
     const int64_t step = (int64_t)(gridDim.x - p.inner_ctas) * gridDim.y * blockDim.x;
     const int64_t first =
         ((int64_t)(blockIdx.x - p.inner_ctas) * gridDim.y + blockIdx.y) * blockDim.x + tid;
-    // rows without an adapter are in no group
-    for (int64_t i = first; p.row && p.u_out && i < (int64_t)p.T * p.r; i += step)
+    // rows without an adapter
+    for (int64_t i = first; p.zero_u && i < (int64_t)p.T * p.r; i += step)
         if ((unsigned)__ldg(&p.adapter[i / p.r]) >= (unsigned)p.n)
             p.u_out[i] = 0.0f;
-    for (int64_t i = first; i < p.zero_n; i += step)
-        p.zero[i] = 0;
-    for (int64_t i = first; p.conv && i < all; i += step) {
-        const int t = (int)(i / rp), j = (int)(i % rp);
-        ad_put_parts(p.conv_parts, rp, t, j, j < p.r ? p.conv[(size_t)t * p.r + j] : 0.0f);
+    // eight ranks of a row at a time
+    for (int64_t i = first; p.conv && i < (int64_t)p.T * (rp / 8); i += step) {
+        const int t = (int)(i / (rp / 8)), j = (int)(i % (rp / 8)) * 8;
+        uint16_t q[kAdParts][8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            uint16_t part[kAdParts];
+            split_bf16(j + k < p.r ? __ldg(&p.conv[(size_t)t * p.r + j + k]) : 0.0f, part);
+#pragma unroll
+            for (int h = 0; h < kAdParts; ++h)
+                q[h][k] = part[h];
+        }
+#pragma unroll
+        for (int h = 0; h < kAdParts; ++h)
+            *reinterpret_cast<uint4 *>(&p.conv_parts[((size_t)t * kAdParts + h) * rp + j]) =
+                make_uint4(q[h][0] | (uint32_t)q[h][1] << 16, q[h][2] | (uint32_t)q[h][3] << 16,
+                           q[h][4] | (uint32_t)q[h][5] << 16, q[h][6] | (uint32_t)q[h][7] << 16);
     }
 }
 
-// A tile's rows (st, -1: none) with their adapters (sa), and the distinct
-// ones in order of appearance; all threads of the CTA, which gets their count.
+// A tile's R <= 64 rows (st, -1: none) with their adapters (sa), and the
+// distinct ones in order of appearance; all threads of the CTA, which gets
+// their count.  A warp finds its rows' first ones by a match; a second warp
+// then leaves out what the first has.
 template <int R>
 MOE_DEVINL int ad_tile_list(const AdInnerArgs &p, int i0, int rows, int tid, int *sa, int *st,
-                            int *first_of, int *list, int *count)
+                            int *list, int *count)
 {
-    if (tid < R) {
-        int t = -1, a = -1;
-        if (tid < rows) {
+    const int lane = tid & 31;
+    int a = -1;
+    unsigned firsts = 0u;
+    bool first = false;
+    if (tid < (R + 31) / 32 * 32) {
+        int t = -1;
+        if (tid < min(rows, R)) {
             t = p.row ? __ldcg(&p.row[i0 + tid]) : i0 + tid;
             if ((unsigned)t < (unsigned)p.T)
                 a = adapter_of(p.adapter, t, p.n, p.status);
             else
                 t = -1;
         }
-        st[tid] = t;
-        sa[tid] = a;
+        if (tid < R) {
+            st[tid] = t;
+            sa[tid] = a;
+        }
+        const unsigned same = __match_any_sync(0xffffffffu, a);
+        first = a >= 0 && (int)__ffs(same) - 1 == lane;
+        firsts = __ballot_sync(0xffffffffu, first);
+        if (tid < 32) {
+            if (first)
+                list[__popc(firsts & ((1u << lane) - 1u))] = a;
+            if (lane == 0)
+                *count = __popc(firsts);
+        }
     }
     __syncthreads();
-    if (tid < R) {
-        bool first = sa[tid] >= 0;
-        for (int i = 0; i < tid; ++i)
-            first &= sa[i] != sa[tid];
-        first_of[tid] = first;
+    if (R > 32) {
+        const int have = *count;
+        if (tid >= 32 && tid < 64) {
+            for (int i = 0; i < have; ++i)
+                first = first && list[i] != a;
+            firsts = __ballot_sync(0xffffffffu, first);
+        }
+        __syncthreads();
+        if (tid >= 32 && tid < 64) {
+            if (first)
+                list[have + __popc(firsts & ((1u << lane) - 1u))] = a;
+            if (lane == 0)
+                *count = have + __popc(firsts);
+        }
+        __syncthreads();
     }
-    __syncthreads();
-    if (tid < R) {
-        int before = 0;
-        for (int i = 0; i < tid; ++i)
-            before += first_of[i];
-        if (first_of[tid])
-            list[before] = sa[tid];
-        if (tid == R - 1)
-            *count = before + first_of[tid];
-    }
-    __syncthreads();
     return *count;
 }
 
-// One CTA for 16 MT rows, 8 NT ranks (blockIdx.y) and every lists-th of the
+// One CTA for 16 rows, 8 NT ranks (blockIdx.y) and every lists-th of the
 // rows' distinct adapters.  Its warps take the chunks of K in turn, so the
 // CTA reads whole 512-byte pieces of its rows, and add up through shared
 // memory.  A pass over K for each distinct adapter computes all rows and
 // keeps those that are its own: rows of one request mostly stand together,
 // so a tile has one or two adapters; where every row has another (a decode
 // batch), the lists spread the adapters, whose matrices have to be read
-// anyway, over CTAs.  Bound by the reads of x and of the adapters, once for
-// each tile that has them: more rows to a tile as soon as the tiles still
-// fill the device.
-template <int MT, int NT>
-__global__ void __launch_bounds__(kAdWarps * 32, MT * NT >= 8 ? 1 : 2) k_ad_inner(AdInnerArgs p)
+// anyway, over CTAs.  Bound by the reads of x and of the adapters.
+template <int NT>
+__global__ void __launch_bounds__(kAdWarps * 32, NT >= 8 ? 1 : 2) k_ad_inner(AdInnerArgs p)
 {
-    constexpr int kRows = 16 * MT;
+    constexpr int MT = 1, kRows = 16;
     __shared__ float red[kAdWarps / 2][kRows][8 * NT + 1];
     __shared__ int sa[kRows], st[kRows];  // adapter and row
-    __shared__ int s_first[kRows], s_list[kRows];
+    __shared__ int s_list[kRows];
     __shared__ int s_count;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, q = lane & 3;
@@ -231,7 +255,7 @@ __global__ void __launch_bounds__(kAdWarps * 32, MT * NT >= 8 ? 1 : 2) k_ad_inne
     const int rows = min(kRows, (p.row ? __ldcg(p.rows) : p.T) - i0);
     if (rows <= 0)
         return;
-    const int count = ad_tile_list<kRows>(p, i0, rows, tid, sa, st, s_first, s_list, &s_count);
+    const int count = ad_tile_list<kRows>(p, i0, rows, tid, sa, st, s_list, &s_count);
     const int nc = (p.din + kAdChunk - 1) / kAdChunk;
     const uint16_t *xr[2 * MT];
     bool has[2 * MT];
@@ -250,7 +274,7 @@ __global__ void __launch_bounds__(kAdWarps * 32, MT * NT >= 8 ? 1 : 2) k_ad_inne
             for (int i = 0; i < NT; ++i)
                 acc[m][i][0] = acc[m][i][1] = acc[m][i][2] = acc[m][i][3] = 0.0f;
         const uint16_t *ap = p.a + ((size_t)a * p.r + j0 + g) * p.din;
-#pragma unroll(MT * NT <= 2 ? 8 : MT * NT <= 8 ? 4 : MT * NT <= 16 ? 2 : 1)
+#pragma unroll(NT <= 2 ? 8 : 4)
         for (int c = warp; c < nc; c += kAdWarps) {
             const int k = c * kAdChunk + 8 * q;
             uint4 u[2 * MT];
@@ -313,30 +337,30 @@ __global__ void __launch_bounds__(kAdWarps * 32, MT * NT >= 8 ? 1 : 2) k_ad_inne
     }
 }
 
-// The same for many rows (8 NT >= r of blockIdx.y): 64 rows a CTA and every
-// lists-th of their adapters, one after another.  x and A_a stream through
-// shared memory in stages of 128 values of K, four deep, by asynchronous
-// copies that gather the rows; a warp multiplies 16 rows with half of the
-// ranks over half of a stage, all its fragments loaded before the first
-// product (a few warps hide little latency).  Bound by the read of x (an
-// adapter's matrix is read once for each 64 rows that have it).
+// The same for many rows (8 NT >= r of blockIdx.y): R = 32 or 64 rows a CTA
+// and every lists-th of their adapters, one after another.  x and A_a stream
+// through shared memory in stages of 128 values of K, four deep, by
+// asynchronous copies that gather the rows; a warp multiplies 16 rows with
+// half of the ranks over a part of a stage, all its fragments loaded before
+// the first product (a few warps hide little latency).  Bound by the read of
+// x (an adapter's matrix is read once for each R rows that have it).
 constexpr int kAdBigWarps = 16;
 
-template <int NT>
+template <int NT, int R>
 struct AdBigShape {
-    static constexpr int kRows = 64, kK = 128, kStages = 4;
+    static constexpr int kRows = R, kK = 128, kStages = 4;
     static constexpr int kPitch = kK * 2 + 16;  // bytes; 16 over: rows on other banks
     static constexpr int kStage = (kRows + 8 * NT) * kPitch;
     static constexpr int kBytes = kStages * kStage;
     static constexpr int kRedPitch = 8 * NT + 1;  // the halves' sums, in the stages' place
 };
 
-template <int NT>
+template <int NT, int R>
 __global__ void __launch_bounds__(kAdBigWarps * 32) k_ad_inner_big(AdInnerArgs p)
 {
-    using S = AdBigShape<NT>;
+    using S = AdBigShape<NT, R>;
     extern __shared__ __align__(16) uint8_t ab_smem[];
-    __shared__ int sa[S::kRows], st[S::kRows], s_first[S::kRows], s_list[S::kRows];
+    __shared__ int sa[S::kRows], st[S::kRows], s_list[S::kRows];
     __shared__ int s_count;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rp = ad_rp(p.r);
@@ -352,28 +376,29 @@ __global__ void __launch_bounds__(kAdBigWarps * 32) k_ad_inner_big(AdInnerArgs p
     const int rows = min(S::kRows, (p.row ? __ldcg(p.rows) : p.T) - i0);
     if (rows <= 0)
         return;
-    const int count = ad_tile_list<S::kRows>(p, i0, rows, tid, sa, st, s_first, s_list, &s_count);
+    const int count = ad_tile_list<S::kRows>(p, i0, rows, tid, sa, st, s_list, &s_count);
     const uint32_t sm = smem_addr(ab_smem);
     float *red = reinterpret_cast<float *>(ab_smem);
     const int ns = (p.din + S::kK - 1) / S::kK;
-    const int mt = warp & 3, nh = (warp >> 2) & 1, kh = warp >> 3;  // 16 rows, half the ranks, half of K
-    constexpr int NH = NT / 2, KS = S::kK / 32;                     // instructions' K steps
+    constexpr int kMT = R / 16, kKG = kAdBigWarps / (2 * kMT);  // row tiles, parts of a stage
+    constexpr int NH = NT / 2, KS = S::kK / 16 / kKG;           // instructions of N and of K
+    const int mt = warp % kMT, nh = warp / kMT % 2, kh = warp / (2 * kMT);
     // this thread's vectors of a stage: column ck of rows tid / 16, + 32 of x,
     // then of the adapter; nullptr: zeros
-    constexpr int kVec = 2 + (NT + 3) / 4;
+    constexpr int kXV = R / 32, kVec = kXV + (NT + 3) / 4;
     const int ck = (tid & 15) * 8, r0 = tid >> 4;
     const uint32_t to0 = sm + r0 * S::kPitch + ck * 2;
     const uint16_t *src[kVec];
 #pragma unroll
-    for (int v = 0; v < 2; ++v) {
+    for (int v = 0; v < kXV; ++v) {
         const int t = st[r0 + 32 * v];
         src[v] = t >= 0 ? p.x + (size_t)t * p.din + ck : nullptr;
     }
     for (int l = part; l < count; l += p.lists) {
         const int a = s_list[l];
 #pragma unroll
-        for (int v = 2; v < kVec; ++v) {
-            const int j = j0 + r0 + 32 * (v - 2);
+        for (int v = kXV; v < kVec; ++v) {
+            const int j = j0 + r0 + 32 * (v - kXV);
             src[v] = j < p.r && j < j0 + 8 * NT ? p.a + ((size_t)a * p.r + j) * p.din + ck : nullptr;
         }
         auto issue = [&](int s) {
@@ -402,7 +427,7 @@ __global__ void __launch_bounds__(kAdBigWarps * 32) k_ad_inner_big(AdInnerArgs p
             cp_async_wait<S::kStages - 2>();
             __syncthreads();
             issue(s + S::kStages - 1);
-            const uint32_t at = sm + (s % S::kStages) * S::kStage + kh * S::kK;
+            const uint32_t at = sm + (s % S::kStages) * S::kStage + kh * KS * 32;
             uint32_t x[KS][4], w[KS][NH == 1 ? 1 : NH / 2][4];
 #pragma unroll
             for (int kk = 0; kk < KS; ++kk) {
@@ -433,17 +458,18 @@ __global__ void __launch_bounds__(kAdBigWarps * 32) k_ad_inner_big(AdInnerArgs p
         }
         cp_async_wait<0>();
         __syncthreads();
-        // the halves of K meet
-        if (kh == 1) {
+        // the parts of K meet
+        if (kh > 0) {
+            float *mine = red + (kh - 1) * R * S::kRedPitch;
 #pragma unroll
             for (int i = 0; i < NH; ++i)
 #pragma unroll
                 for (int h = 0; h < 4; ++h)
-                    red[(mt * 16 + (lane >> 2) + 8 * (h >> 1)) * S::kRedPitch + nh * 8 * NH + i * 8 +
+                    mine[(mt * 16 + (lane >> 2) + 8 * (h >> 1)) * S::kRedPitch + nh * 8 * NH + i * 8 +
                         2 * (lane & 3) + (h & 1)] = acc[i][h];
         }
         __syncthreads();
-        if (kh == 1)
+        if (kh > 0)
             continue;
         const float sc = p.scale ? __ldg(&p.scale[a]) : 1.0f;
 #pragma unroll
@@ -458,10 +484,15 @@ __global__ void __launch_bounds__(kAdBigWarps * 32) k_ad_inner_big(AdInnerArgs p
                 if (j >= rp)
                     continue;
                 // two ranks side by side (rp is even)
-                const float *other = red + row * S::kRedPitch + jj;
+                float v0 = acc[i][2 * h], v1 = acc[i][2 * h + 1];
+#pragma unroll
+                for (int k = 0; k < kKG - 1; ++k) {
+                    v0 += red[(k * R + row) * S::kRedPitch + jj];
+                    v1 += red[(k * R + row) * S::kRedPitch + jj + 1];
+                }
+                v0 = j < p.r ? v0 * sc : 0.0f;
+                v1 = j + 1 < p.r ? v1 * sc : 0.0f;
                 uint16_t q0[kAdParts], q1[kAdParts];
-                const float v0 = j < p.r ? (acc[i][2 * h] + other[0]) * sc : 0.0f;
-                const float v1 = j + 1 < p.r ? (acc[i][2 * h + 1] + other[1]) * sc : 0.0f;
                 split_bf16(v0, q0);
                 split_bf16(v1, q1);
 #pragma unroll
@@ -505,6 +536,7 @@ __global__ void __launch_bounds__(kAdGroupWarps * 32) k_ad_group(const int32_t *
     const int t0 = warp * run + lane;
     constexpr int kIds = kAdGroupMaxT / (kAdGroupWarps * 32);
     int id[kIds];  // every row of the run at once
+    unsigned same[kIds];
 #pragma unroll
     for (int i = 0; i < kIds; ++i)
         id[i] = 32 * i < run && t0 + 32 * i < T ? __ldg(&adapter[t0 + 32 * i]) : MOE_EMPTY_SLOT;
@@ -517,9 +549,9 @@ __global__ void __launch_bounds__(kAdGroupWarps * 32) k_ad_group(const int32_t *
                 set_status(status, MOE_ERR_DEVICE_CHECK);
             id[i] = -1;
         }
-        const unsigned same = __match_any_sync(0xffffffffu, id[i]);
-        if (id[i] >= 0 && (int)__ffs(same) - 1 == lane)
-            sg[id[i] * (kAdGroupWarps + 1) + warp] += __popc(same);
+        same[i] = __match_any_sync(0xffffffffu, id[i]);
+        if (id[i] >= 0 && (int)__ffs(same[i]) - 1 == lane)
+            sg[id[i] * (kAdGroupWarps + 1) + warp] += __popc(same[i]);
         __syncwarp();
     }
     __syncthreads();
@@ -545,15 +577,14 @@ __global__ void __launch_bounds__(kAdGroupWarps * 32) k_ad_group(const int32_t *
         if (32 * i >= run)
             break;
         const int a = id[i];
-        const unsigned same = __match_any_sync(0xffffffffu, a);
         int base = 0;
         if (a >= 0)
             base = start[a] + sg[a * (kAdGroupWarps + 1) + warp];
         __syncwarp();
         if (a >= 0) {
-            row[base + __popc(same & ((1u << lane) - 1u))] = t0 + 32 * i;
-            if ((int)__ffs(same) - 1 == lane)
-                sg[a * (kAdGroupWarps + 1) + warp] += __popc(same);
+            row[base + __popc(same[i] & ((1u << lane) - 1u))] = t0 + 32 * i;
+            if ((int)__ffs(same[i]) - 1 == lane)
+                sg[a * (kAdGroupWarps + 1) + warp] += __popc(same[i]);
         }
         __syncwarp();
     }
@@ -574,6 +605,8 @@ struct AdProductArgs {
     void *y;                 // [T x dout]
     int y_bf16;
     int T, din, dout, r, n;
+    int splits;              // k_ad_gemm: parts of K; above 1 their sums go to partial
+    float *partial;          // [tiles][splits][256 x kAGSplitCols]
     WsHeader *hdr;
 };
 
@@ -824,250 +857,6 @@ __global__ void __launch_bounds__(kAdWarps * 32) k_ad_rows(AdProductArgs p, AdOn
             }
             *y = make_float2(o[0], o[1]);
         }
-    }
-}
-
-// ---------------------------------------------------------------------------
-// Sums of outer products: g[a][j][c] = sum_{t of a} u[t][j] z[t][c], for two
-// problems (dA from v and x, dB from u and dy) over one grouping of the rows.
-struct AdOuterProblem {
-    const uint16_t *parts;  // [T][kAdParts][rp]
-    const uint16_t *z;      // [T x D]
-    float *g;               // [n x r x D]; nullptr: no such problem
-    int D;
-};
-struct AdOuterArgs {
-    AdOuterProblem pr[2];
-    int dch0;                // column blocks of problem 0
-    const int32_t *offsets;  // [n + 1] rows grouped by adapter (the counting sort)
-    const int32_t *row;      // [offsets[n]]
-    float *partial;          // pieces of adapters with several
-    int *arrive;             // [n x column blocks x rank blocks], cleared by the inner step
-    int rows;                // rows of one piece
-    int T, r, n;
-    int *status;
-};
-
-constexpr int kAdOutCols = 128;  // columns of a CTA: 16 for each of 8 warps
-constexpr int kAdOutRows = 32;   // rows of a stage
-constexpr int kAdOutStages = 4;
-constexpr int kAdOutZPitch = kAdOutCols * 2 + 16;  // bytes; 16 over: rows on other banks
-template <int MT>
-struct AdOuterSmem {
-    static constexpr int kUPitch = MT * 32 + 16;
-    static constexpr int kStage = kAdOutRows * (kAdOutZPitch + kAdParts * kUPitch);
-    static constexpr int kBytes = kAdOutStages * kStage;
-};
-
-// A CTA sums one piece (up to `rows` rows of one adapter) for 128 columns and
-// 16 MT ranks (blockIdx.z): u^T is the M side and z the N side of the matrix
-// instruction, K runs over the rows, which arrive by asynchronous copies four
-// stages deep and are transposed on the way to registers.  Adapters of one
-// piece are stored at once; the pieces of larger ones meet in scratch, where
-// the last to arrive adds them in order, so results do not depend on timing.
-// The pieces are found from the offsets on the device (the host knows only
-// T): blockIdx.x counts them, adapters without rows have one that stores
-// zeros, and CTAs behind the last leave.  Bound by the read of z.
-template <int MT>
-__global__ void __launch_bounds__(256) k_ad_outer(AdOuterArgs p)
-{
-    extern __shared__ __align__(16) uint8_t ao_smem[];
-    __shared__ int s_item[6];  // adapter, first row, rows, pieces, first scratch piece, piece
-    __shared__ int s_scan[32];
-    __shared__ int s_last;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    pdl_wait();
-    pdl_trigger();
-    const int which = (int)blockIdx.y >= p.dch0;
-    const AdOuterProblem pr = which ? p.pr[1] : p.pr[0];
-    const int cb = blockIdx.y - (which ? p.dch0 : 0);
-    const int rp = ad_rp(p.r);
-    const int j0 = blockIdx.z * 16 * MT;
-
-    // which piece: pieces before adapter e, and scratch pieces before it
-    if (tid == 0)
-        s_item[0] = -1;
-    __syncthreads();
-    {
-        int base = 0, sbase = 0;
-        for (int e0 = 0; e0 < p.n; e0 += 256) {
-            const int e = e0 + tid;
-            int first = 0, len = 0, np = 0;
-            if (e < p.n) {
-                first = __ldcg(&p.offsets[e]);
-                len = __ldcg(&p.offsets[e + 1]) - first;
-                np = len > p.rows ? (len + p.rows - 1) / p.rows : 1;
-            }
-            // scans of the pieces and of those that go through scratch
-            int v = np, s = np > 1 ? np : 0;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int a = __shfl_up_sync(0xffffffffu, v, o), b = __shfl_up_sync(0xffffffffu, s, o);
-                if (lane >= o) {
-                    v += a;
-                    s += b;
-                }
-            }
-            if (lane == 31) {
-                s_scan[warp] = v;
-                s_scan[16 + warp] = s;
-            }
-            __syncthreads();
-            int wv = 0, wsum = 0, tv = 0, ts = 0;
-            for (int w = 0; w < 8; ++w) {
-                if (w < warp) {
-                    wv += s_scan[w];
-                    wsum += s_scan[16 + w];
-                }
-                tv += s_scan[w];
-                ts += s_scan[16 + w];
-            }
-            const int start = base + wv + v - np;
-            const int i = blockIdx.x;
-            if (e < p.n && i >= start && i < start + np) {
-                s_item[0] = e;
-                s_item[5] = i - start;
-                s_item[1] = first + s_item[5] * p.rows;
-                s_item[2] = min(p.rows, len - s_item[5] * p.rows);
-                s_item[3] = np;
-                s_item[4] = sbase + wsum + s - (np > 1 ? np : 0);
-            }
-            base += tv;
-            sbase += ts;
-            __syncthreads();
-            if (s_item[0] >= 0 || base > (int)blockIdx.x)
-                break;
-        }
-    }
-    const int a = s_item[0];
-    if (a < 0)
-        return;
-    const int first = s_item[1], len = s_item[2], pieces = s_item[3];
-
-    constexpr int kUP = AdOuterSmem<MT>::kUPitch, kStage = AdOuterSmem<MT>::kStage;
-    const uint32_t sm = smem_addr(ao_smem);
-    const int ns = (len + kAdOutRows - 1) / kAdOutRows;
-    auto issue = [&](int s) {
-        if (s < ns) {
-            const uint32_t st = sm + (s % kAdOutStages) * kStage;
-            // z: 32 rows x 16 vectors; u: 32 rows x 3 parts x 2 MT vectors
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int i = tid + 256 * h, rr = i >> 4, c = i & 15;
-                const int m = s * kAdOutRows + rr;
-                const int col = cb * kAdOutCols + c * 8;
-                int t = 0;
-                bool live = m < len;
-                if (live)
-                    t = __ldg(&p.row[first + m]);
-                live = live && (unsigned)t < (unsigned)p.T;
-                cp_async16(st + rr * kAdOutZPitch + c * 16,
-                           pr.z + (live && col < pr.D ? (size_t)t * pr.D + col : 0),
-                           live && col < pr.D);
-            }
-            for (int i = tid; i < kAdOutRows * kAdParts * 2 * MT; i += 256) {
-                const int rr = i / (kAdParts * 2 * MT), c = i % (kAdParts * 2 * MT);
-                const int half = c / (2 * MT), v = c % (2 * MT);
-                const int m = s * kAdOutRows + rr;
-                const int j = j0 + v * 8;
-                int t = 0;
-                bool live = m < len && j < rp;
-                if (live)
-                    t = __ldg(&p.row[first + m]);
-                live = live && (unsigned)t < (unsigned)p.T;
-                cp_async16(st + kAdOutRows * (kAdOutZPitch + half * kUP) + rr * kUP + v * 16,
-                           pr.parts + (live ? ((size_t)t * kAdParts + half) * rp + j : 0), live);
-            }
-        }
-        cp_async_commit();
-    };
-    float acc[MT][2][4];
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-            acc[m][i][0] = acc[m][i][1] = acc[m][i][2] = acc[m][i][3] = 0.0f;
-#pragma unroll
-    for (int s = 0; s < kAdOutStages - 1; ++s)
-        issue(s);
-    for (int s = 0; s < ns; ++s) {
-        cp_async_wait<kAdOutStages - 2>();
-        __syncthreads();
-        issue(s + kAdOutStages - 1);
-        const uint32_t st = sm + (s % kAdOutStages) * kStage;
-#pragma unroll
-        for (int kk = 0; kk < kAdOutRows / 16; ++kk) {
-            // z: four 8 x 8 blocks -- rows 0-7 and 8-15 of columns 0-7, then of 8-15
-            uint32_t b[4];
-            ldmatrix_x4_t(st + (kk * 16 + (lane & 15)) * kAdOutZPitch +
-                              (warp * 16 + (lane >> 4) * 8) * 2,
-                          b);
-#pragma unroll
-            for (int half = 0; half < kAdParts; ++half)
-#pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    // u^T: ranks 0-7 and 8-15 of rows 0-7, then of rows 8-15
-                    uint32_t u[4];
-                    ldmatrix_x4_t(st + kAdOutRows * (kAdOutZPitch + half * kUP) +
-                                      (kk * 16 + (lane & 7) + (lane >> 4) * 8) * kUP +
-                                      (m * 16 + ((lane >> 3) & 1) * 8) * 2,
-                                  u);
-                    mma_bf16(acc[m][0], u[0], u[1], u[2], u[3], b[0], b[1]);
-                    mma_bf16(acc[m][1], u[0], u[1], u[2], u[3], b[2], b[3]);
-                }
-        }
-    }
-    cp_async_wait<0>();
-
-    const int gq = lane >> 2, q = lane & 3;
-    const size_t plane = (size_t)p.r * pr.D;
-    float *out = pr.g + (size_t)a * plane;
-    // scratch: pieces of both problems, problem 0's first
-    const size_t plane0 = p.pr[0].g ? (size_t)p.r * p.pr[0].D : 0;
-    const size_t both = plane0 + (p.pr[1].g ? (size_t)p.r * p.pr[1].D : 0);
-    float *mine = nullptr;
-    if (pieces > 1) {
-        mine = p.partial + (size_t)s_item[4] * both + (which ? plane0 : 0);
-        out = mine + (size_t)s_item[5] * both;
-    }
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int j = j0 + m * 16 + gq + 8 * h;
-                const int c = cb * kAdOutCols + warp * 16 + i * 8 + 2 * q;
-                if (j < p.r && c < pr.D)
-                    *reinterpret_cast<float2 *>(out + (size_t)j * pr.D + c) =
-                        make_float2(acc[m][i][2 * h], acc[m][i][2 * h + 1]);
-            }
-    if (pieces == 1)
-        return;
-    __threadfence();
-    __syncthreads();
-    if (tid == 0) {
-        int *cnt = p.arrive + ((size_t)a * gridDim.y + blockIdx.y) * gridDim.z + blockIdx.z;
-        s_last = atomicAdd(cnt, 1) == pieces - 1;
-    }
-    __syncthreads();
-    if (!s_last)
-        return;
-    __threadfence();
-    for (int i = tid; i < 16 * MT * (kAdOutCols / 4); i += 256) {
-        const int j = j0 + i / (kAdOutCols / 4), c = cb * kAdOutCols + (i % (kAdOutCols / 4)) * 4;
-        if (j >= p.r || c >= pr.D)
-            continue;
-        const size_t o = (size_t)j * pr.D + c;
-        float4 s = __ldcg(reinterpret_cast<const float4 *>(mine + o));
-        for (int k = 1; k < pieces; ++k) {
-            const float4 v = __ldcg(reinterpret_cast<const float4 *>(mine + k * both + o));
-            s.x += v.x;
-            s.y += v.y;
-            s.z += v.z;
-            s.w += v.w;
-        }
-        *reinterpret_cast<float4 *>(pr.g + (size_t)a * plane + o) = s;
     }
 }
 

@@ -18,6 +18,12 @@
 // the epilogue computes an output that came out NaN once more, alone, from
 // its own row and adapter.
 //
+// Where the tiles leave more than half of the pairs idle (few rows, or few
+// outputs as a router has), K is split over several pairs, which leave their
+// float32 sums in scratch; k_ad_join adds them in order and stores y (on all
+// SMs, where the last CTA to arrive alone would wait for its reads longer
+// than the split saves: 35 against 25 us for 4096 rows, 2048 to 128).
+//
 // The two CTAs of a pair share tiles of 256 rows x BN outputs: each holds its
 // 128 rows of X and half of the outputs' rows of W in shared memory, and the
 // accumulators of its 128 rows (two sets of BN columns, so the epilogue of
@@ -103,6 +109,11 @@ MOE_DEVINL void mbar_expect_tx(uint64_t *bar, uint32_t bytes)
                  : "memory");
 }
 
+MOE_DEVINL void prefetch_tensormap(const CUtensorMap *m)
+{
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
+}
+
 MOE_DEVINL bool ag_aborted(const AGSync &sy) { return *(volatile const int *)&sy.abort != 0; }
 
 // One output alone, in float32: the row's product with W (or what y holds)
@@ -120,6 +131,61 @@ __device__ __noinline__ float ag_one(const AdProductArgs &p, int a, int t, int o
         }
     }
     return a >= 0 ? v + ad_part(p, a, t, o) : v;
+}
+
+MOE_DEVINL uint32_t ag_word(uint32_t w) { return w; }
+MOE_DEVINL uint32_t ag_word(float w) { return __float_as_uint(w); }
+
+// A lane holds N words of its own row (of 32 rows); four lanes (a quad)
+// exchange vectors of four words so that vector 4 b + c of a lane becomes
+// vector 4 b + (lane % 4) of the quad's row c: a store then writes 64 bytes of
+// a row from a quad, whole sectors, where each lane's own row would give 32
+// rows 16 bytes each.
+template <int N, typename W>
+MOE_DEVINL void ag_quad_rows(W (&v)[N])
+{
+    const int q = threadIdx.x & 3;
+#pragma unroll
+    for (int b = 0; b < N; b += 16) {
+        // 4 x 4 transpose of vectors: halves across lanes 2 apart, then neighbours
+#pragma unroll
+        for (int s = 2; s >= 1; s >>= 1)
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                if (!(c & s))
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        W &lo = v[b + 4 * c + k], &hi = v[b + 4 * (c | s) + k];
+                        const W give = q & s ? lo : hi;
+                        const W got = __shfl_xor_sync(0xffffffffu, give, s);
+                        if (q & s)
+                            lo = got;
+                        else
+                            hi = got;
+                    }
+    }
+}
+
+// Store what ag_quad_rows arranged: columns o .. o + 31 of rows r0 .. r0 + 31
+// (below rows) of a matrix whose rows are ld values; columns below cols.
+template <typename E, int N, typename W>
+MOE_DEVINL void ag_put(E *base, int ld, int o, int r0, int lane, int rows, int cols, const W (&v)[N])
+{
+    constexpr int kPer = 16 / sizeof(E);  // values of a vector
+#pragma unroll
+    for (int b = 0; b < N; b += 16)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const int row = r0 + (lane & ~3) + c, col = o + (b / 4 + (lane & 3)) * kPer;
+            if (row < rows && col < cols) {
+                uint4 q;
+                q.x = ag_word(v[b + 4 * c]);
+                q.y = ag_word(v[b + 4 * c + 1]);
+                q.z = ag_word(v[b + 4 * c + 2]);
+                q.w = ag_word(v[b + 4 * c + 3]);
+                *reinterpret_cast<uint4 *>(base + (size_t)row * ld + col) = q;
+            }
+        }
 }
 
 template <int BN>
@@ -155,6 +221,28 @@ __global__ void __launch_bounds__(kAGThreads, 1)
         sy.abort = 0;
         fence_mbar_init();
     }
+    // U warps: the first tile's adapters, on their way during the set-up
+    const int splits = p.splits;
+    const int ncol = (p.dout + BN - 1) / BN, nrow = (p.T + kAGRows - 1) / kAGRows;
+    // work items: (tile, split), the splits of a tile side by side
+    const int items = nrow * ncol * splits, pairs = gridDim.x / 2, pair = blockIdx.x / 2;
+    const int ut = tid - kAGWarpU * 32;  // U warps: this CTA's row of the tile
+    int a_own = -1, a_peer = -1;
+    auto load_ids = [&](int it) {
+        const int t = it / splits / ncol * kAGRows + (int)rank * 128 + ut;
+        const int tp = it / splits / ncol * kAGRows + (int)peer * 128 + ut;
+        a_own = t < p.T ? adapter_of(p.adapter, t, p.n, status) : -1;
+        a_peer = tp < p.T ? adapter_of(p.adapter, tp, p.n, status) : -1;
+    };
+    if (warp >= kAGWarpU && pair < items)
+        load_ids(pair);
+    if (warp == kGWarpTma && lane == 0) {
+        if (p.w) {
+            prefetch_tensormap(&tm_x);
+            prefetch_tensormap(&tm_w);
+        }
+        prefetch_tensormap(&tm_b);
+    }
     if (warp == kGWarpMma) {
         tmem_alloc_pair(&sy.tmem_base, 2 * BN);
         tmem_relinquish_pair();
@@ -166,17 +254,17 @@ __global__ void __launch_bounds__(kAGThreads, 1)
     const uint32_t tmem = sy.tmem_base;
 
     const int nkb = p.w ? (p.din + kGBK - 1) / kGBK : 0;
-    const int ncol = (p.dout + BN - 1) / BN, nrow = (p.T + kAGRows - 1) / kAGRows;
-    const int tiles = nrow * ncol, pairs = gridDim.x / 2, pair = blockIdx.x / 2;
+    const int nks = (nkb + splits - 1) / splits;  // K blocks of a split
     const int nch = ad_rp(p.r) / 16;  // units of an adapter
 
     if (warp == kGWarpTma) {
         if (lane == 0) {
             uint32_t g = 0;
-            for (int i = pair; i < tiles && !ag_aborted(sy); i += pairs) {
+            for (int it = pair; it < items && !ag_aborted(sy); it += pairs) {
+                const int i = it / splits, kb0 = it % splits * nks, kb1 = min(nkb, kb0 + nks);
                 const int t0 = i / ncol * kAGRows + (int)rank * 128;
                 const int o0 = i % ncol * BN + (int)rank * (BN / 2);
-                for (int kb = 0; kb < nkb; ++kb, ++g) {
+                for (int kb = kb0; kb < kb1; ++kb, ++g) {
                     const int s = g % S::kStages;
                     if (!mbar_wait_cluster(&sy.empty[s], ((g / S::kStages) & 1) ^ 1, status)) {
                         sy.abort = 1;
@@ -200,8 +288,9 @@ __global__ void __launch_bounds__(kAGThreads, 1)
             uint32_t g = 0, ub = 0, itc = 0;
             const uint32_t idesc = umma_idesc_bf16(kAGRows, BN);
             const uint32_t idesc_mn = idesc | (1u << 16);  // B along N
-            for (int i = pair; i < tiles; i += pairs, ++itc) {
+            for (int it = pair; it < items; it += pairs, ++itc) {
                 const int buf = itc & 1;
+                const int kb0 = it % splits * nks, kb1 = min(nkb, kb0 + nks);
                 if (!mbar_wait_cluster(&sy.acc_empty[buf], ((itc >> 1) & 1) ^ 1, status)) {
                     sy.abort = 1;
                     break;
@@ -209,7 +298,7 @@ __global__ void __launch_bounds__(kAGThreads, 1)
                 tc_fence_after();
                 const uint32_t dt = tmem + buf * BN;
                 uint32_t acc = 0;
-                for (int kb = 0; kb < nkb; ++kb, ++g) {
+                for (int kb = kb0; kb < kb1; ++kb, ++g) {
                     const int s = g % S::kStages;
                     if (!mbar_wait_cluster(&sy.full[s], (g / S::kStages) & 1, status)) {
                         sy.abort = 1;
@@ -225,7 +314,7 @@ __global__ void __launch_bounds__(kAGThreads, 1)
                     }
                     umma_commit_pair_both(&sy.empty[s]);
                 }
-                while (!ag_aborted(sy)) {
+                while (it % splits == 0 && !ag_aborted(sy)) {
                     const int b = ub % kAGUBufs;
                     if (!mbar_wait_cluster(&sy.ufull[b], (ub / kAGUBufs) & 1, status)) {
                         sy.abort = 1;
@@ -256,15 +345,18 @@ __global__ void __launch_bounds__(kAGThreads, 1)
         }
     } else if (warp >= kAGWarpU) {
         // ------------------------------------------------------------ U and B
-        const int ut = tid - kAGWarpU * 32;  // this CTA's row of the tile
         const int rp = ad_rp(p.r);
         uint32_t ub = 0;
-        for (int i = pair; i < tiles; i += pairs) {
+        bool waited = false;
+        for (int it = pair; it < items; it += pairs) {
+            if (it % splits)
+                continue;  // the first split takes the adapters
+            const int i = it / splits;
             // the tile's adapters, both CTAs' rows, in order of their number
-            const int tb = i / ncol * kAGRows;
-            const int t = tb + (int)rank * 128 + ut, tp = tb + (int)peer * 128 + ut;
-            const int a = t < p.T ? adapter_of(p.adapter, t, p.n, status) : -1;
-            const int ap = tp < p.T ? adapter_of(p.adapter, tp, p.n, status) : -1;
+            if (it != pair)
+                load_ids(it);
+            const int a = a_own, ap = a_peer;
+            const int t = i / ncol * kAGRows + (int)rank * 128 + ut;
             if (ut < 32)
                 sy.bits[ut] = 0u;
             named_bar_sync(1, 128);
@@ -308,8 +400,26 @@ __global__ void __launch_bounds__(kAGThreads, 1)
                 for (int c = 0; c < 2 * kAdParts; ++c)
                     own[c] = __ldcg(reinterpret_cast<const uint4 *>(urow + c / 2 * rp + j) + c % 2);
             };
-            if (i == pair)
+            // B of unit u (one thread), once its buffer is free
+            auto load_b = [&](int u, int b) {
+                const int e = sy.list[u / nch], j = u % nch * 16;
+                uint8_t *st = ubuf + (size_t)b * S::kUBuf;
+                const uint32_t fb = cluster_addr(&sy.ufull[b], 0);
+                if (lead)
+                    mbar_expect_tx(&sy.ufull[b], 2 * S::kUnitB);
+                for (int c = 0; c < BN / 128; ++c)
+                    tma_load_3d_pair(st + kAGTileA + c * 2048, &tm_b, o0 + 64 * c, j, e, fb);
+            };
+            int ahead = 0;  // units whose B is on its way already: the first buffers' before the wait
+            if (!waited) {
+                ahead = min(units, kAGUBufs);
+                if (ut == 0)
+                    for (int u = 0; u < ahead; ++u)
+                        load_b(u, u);
                 pdl_wait();
+                pdl_trigger();
+                waited = true;
+            }
             if (a >= 0)
                 load_own(0);
             int u0 = 0;
@@ -328,13 +438,8 @@ __global__ void __launch_bounds__(kAGThreads, 1)
                 if (ut == 0) {
                     if (lead)
                         sy.u_what[b] = (e >= 0 ? 1 : 0) | (u0 + 1 >= units ? 2 : 0);
-                    const uint32_t fb = cluster_addr(&sy.ufull[b], 0);
-                    if (e >= 0) {
-                        if (lead)
-                            mbar_expect_tx(&sy.ufull[b], 2 * S::kUnitB);
-                        for (int c = 0; c < BN / 128; ++c)
-                            tma_load_3d_pair(st + kAGTileA + c * 2048, &tm_b, o0 + 64 * c, j, e, fb);
-                    }
+                    if (u0 >= ahead && e >= 0)
+                        load_b(u0, b);
                 }
 #pragma unroll
                 for (int c = 0; c < 2 * kAdParts; ++c)
@@ -359,9 +464,11 @@ __global__ void __launch_bounds__(kAGThreads, 1)
         const uint32_t lane_addr = tmem + ((uint32_t)(lq * 32) << 16);
         uint32_t itc = 0;
         pdl_wait();
-        for (int i = pair; i < tiles; i += pairs, ++itc) {
-            const int buf = itc & 1;
-            const int t = i / ncol * kAGRows + (int)rank * 128 + lq * 32 + lane;
+        pdl_trigger();
+        for (int it = pair; it < items; it += pairs, ++itc) {
+            const int buf = itc & 1, i = it / splits;
+            const int row0 = i / ncol * kAGRows + (int)rank * 128;  // this CTA's first row
+            const int t = row0 + lq * 32 + lane;
             const int o0 = i % ncol * BN;
             int ok = 1;
             if (lane == 0)
@@ -371,6 +478,7 @@ __global__ void __launch_bounds__(kAGThreads, 1)
                 break;
             }
             tc_fence_after();
+            float *part = splits > 1 ? p.partial + ((size_t)it * 2 + rank) * 128 * BN : nullptr;
 #pragma unroll 1
             for (int c = eh; c < BN / 32; c += 2) {
                 const int o = o0 + c * 32;
@@ -379,62 +487,73 @@ __global__ void __launch_bounds__(kAGThreads, 1)
                 float v[32];
                 __syncwarp();
                 tmem_ld32(lane_addr + buf * BN + c * 32, v);
-                if (t >= p.T)
+                if (splits > 1) {
+                    ag_quad_rows(v);
+                    ag_put<float>(part, BN, c * 32, lq * 32, lane, 128, BN, v);
                     continue;
+                }
                 bool bad = false;
 #pragma unroll
                 for (int j = 0; j < 32; ++j)
                     bad |= v[j] != v[j];
-                if (bad) {
+                if (bad && t < p.T) {
                     const int a = adapter_of(p.adapter, t, p.n, nullptr);
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
                         if (v[j] != v[j] && o + j < p.dout)
                             v[j] = ag_one(p, a, t, o + j);
                 }
-                const size_t at = (size_t)t * p.dout + o;
-                // dout % 8 == 0: vectors of eight outputs are whole or absent
+                if (p.bias) {
 #pragma unroll
-                for (int j = 0; j < 32; j += 8) {
-                    if (o + j >= p.dout)
-                        break;
-                    if (p.bias) {
+                    for (int j = 0; j < 32; j += 8)
+                        if (o + j < p.dout)
 #pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            v[j + k] += __ldg(&p.bias[o + j + k]);
-                    }
-                    if (p.y_bf16) {
-                        uint4 *y = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.y) + at + j);
-                        if (!p.w) {
-                            const uint4 old = *y;
-                            v[j] += bf16lo(old.x);
-                            v[j + 1] += bf16hi(old.x);
-                            v[j + 2] += bf16lo(old.y);
-                            v[j + 3] += bf16hi(old.y);
-                            v[j + 4] += bf16lo(old.z);
-                            v[j + 5] += bf16hi(old.z);
-                            v[j + 6] += bf16lo(old.w);
-                            v[j + 7] += bf16hi(old.w);
-                        }
-                        *y = make_uint4(pack_bf16x2(v[j], v[j + 1]), pack_bf16x2(v[j + 2], v[j + 3]),
-                                        pack_bf16x2(v[j + 4], v[j + 5]),
-                                        pack_bf16x2(v[j + 6], v[j + 7]));
+                            for (int k = 0; k < 8; ++k)
+                                v[j + k] += __ldg(&p.bias[o + j + k]);
+                }
+                __syncwarp();
+                if (p.y_bf16) {
+                    uint32_t h[16];
+                    if (p.w) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            h[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
                     } else {
-                        float4 *y = reinterpret_cast<float4 *>(static_cast<float *>(p.y) + at + j);
+                        const uint4 *old = reinterpret_cast<const uint4 *>(
+                            static_cast<const uint16_t *>(p.y) + (size_t)t * p.dout + o);
 #pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            float4 n = make_float4(v[j + 4 * k], v[j + 4 * k + 1], v[j + 4 * k + 2],
-                                                   v[j + 4 * k + 3]);
-                            if (!p.w) {
-                                const float4 old = y[k];
-                                n.x += old.x;
-                                n.y += old.y;
-                                n.z += old.z;
-                                n.w += old.w;
-                            }
-                            y[k] = n;
+                        for (int j = 0; j < 16; j += 4) {
+                            uint4 w = make_uint4(0u, 0u, 0u, 0u);
+                            if (t < p.T && o + 2 * j < p.dout)
+                                w = old[j / 4];
+                            h[j] = pack_bf16x2(v[2 * j] + bf16lo(w.x), v[2 * j + 1] + bf16hi(w.x));
+                            h[j + 1] = pack_bf16x2(v[2 * j + 2] + bf16lo(w.y), v[2 * j + 3] + bf16hi(w.y));
+                            h[j + 2] = pack_bf16x2(v[2 * j + 4] + bf16lo(w.z), v[2 * j + 5] + bf16hi(w.z));
+                            h[j + 3] = pack_bf16x2(v[2 * j + 6] + bf16lo(w.w), v[2 * j + 7] + bf16hi(w.w));
                         }
                     }
+                    __syncwarp();
+                    ag_quad_rows(h);
+                    ag_put<uint16_t>(static_cast<uint16_t *>(p.y), p.dout, o, row0 + lq * 32, lane, p.T,
+                                     p.dout, h);
+                } else {
+                    if (!p.w) {
+                        const float4 *old = reinterpret_cast<const float4 *>(
+                            static_cast<const float *>(p.y) + (size_t)t * p.dout + o);
+#pragma unroll
+                        for (int j = 0; j < 32; j += 4)
+                            if (t < p.T && o + j < p.dout) {
+                                const float4 w = old[j / 4];
+                                v[j] += w.x;
+                                v[j + 1] += w.y;
+                                v[j + 2] += w.z;
+                                v[j + 3] += w.w;
+                            }
+                    }
+                    __syncwarp();
+                    ag_quad_rows(v);
+                    ag_put<float>(static_cast<float *>(p.y), p.dout, o, row0 + lq * 32, lane, p.T, p.dout,
+                                  v);
                 }
             }
             tc_fence_before();
@@ -447,7 +566,6 @@ __global__ void __launch_bounds__(kAGThreads, 1)
     // shared memory goes away while the other may still reach it
     tc_fence_before();
     __syncthreads();
-    pdl_trigger();
     if (warp == kGWarpMma) {
         if (lane == 0 && !lead)
             mbar_wait(&sy.drained, 0, status);
@@ -458,6 +576,65 @@ __global__ void __launch_bounds__(kAGThreads, 1)
     if (tid == 0) {
         mbar_arrive_cluster(cluster_addr(&sy.bye, peer));
         mbar_wait_cluster(&sy.bye, 0, status);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// y from the splits' sums: eight outputs of a row a thread, all splits' loads
+// in flight, added in order of the splits.
+constexpr int kAGSplitCols = 128;  // BN where K is split
+constexpr int kAGMaxSplits = 8;
+
+__global__ void __launch_bounds__(256) k_ad_join(AdProductArgs p)
+{
+    pdl_wait();
+    pdl_trigger();
+    const int nv = p.dout / 8, ncol = (p.dout + kAGSplitCols - 1) / kAGSplitCols;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= (int64_t)p.T * nv)
+        return;
+    const int t = (int)(i / nv), o = (int)(i % nv) * 8;
+    const size_t tile = (size_t)(t / kAGRows) * ncol + o / kAGSplitCols;
+    const float *q = p.partial + (tile * p.splits * kAGRows + t % kAGRows) * kAGSplitCols +
+                     o % kAGSplitCols;
+    float4 a[kAGMaxSplits], b[kAGMaxSplits];
+#pragma unroll
+    for (int s = 0; s < kAGMaxSplits; ++s)
+        if (s < p.splits) {
+            const float4 *r =
+                reinterpret_cast<const float4 *>(q + (size_t)s * kAGRows * kAGSplitCols);
+            a[s] = __ldcg(r);
+            b[s] = __ldcg(r + 1);
+        }
+    float v[8] = {};
+#pragma unroll
+    for (int s = 0; s < kAGMaxSplits; ++s)
+        if (s < p.splits) {
+            v[0] += a[s].x;
+            v[1] += a[s].y;
+            v[2] += a[s].z;
+            v[3] += a[s].w;
+            v[4] += b[s].x;
+            v[5] += b[s].y;
+            v[6] += b[s].z;
+            v[7] += b[s].w;
+        }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        if (v[k] != v[k])
+            v[k] = ag_one(p, adapter_of(p.adapter, t, p.n, nullptr), t, o + k);
+        if (p.bias)
+            v[k] += __ldg(&p.bias[o + k]);
+    }
+    const size_t at = (size_t)t * p.dout + o;
+    if (p.y_bf16) {
+        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.y) + at) =
+            make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                       pack_bf16x2(v[6], v[7]));
+    } else {
+        float4 *y = reinterpret_cast<float4 *>(static_cast<float *>(p.y) + at);
+        y[0] = make_float4(v[0], v[1], v[2], v[3]);
+        y[1] = make_float4(v[4], v[5], v[6], v[7]);
     }
 }
 

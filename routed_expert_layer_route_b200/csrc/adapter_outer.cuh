@@ -1,0 +1,337 @@
+// adapter_outer.cuh -- the adapters' weight gradients on the tensor cores:
+// sums of outer products over each adapter's rows,
+//     g[a][j][c] = sum_{t of a} u[t][j] z[t][c],
+// for two problems (dA from v and x, dB from u and dy) over one grouping of
+// the rows.
+//
+// K runs over the rows, so both operands lie with K outermost (their other
+// index contiguous): the gathered rows of z and of u's three bf16 parts go to
+// shared memory as they are, by asynchronous copies into the 128-byte swizzled
+// layout (blocks of 64 values x 8 rows), and tcgen05.mma reads them transposed.
+// Ranks are the M side (128 lanes of which up to 64 are ranks; the others read
+// the neighbouring block and are not looked at), 256 columns the N side; the
+// three parts of u add up in one accumulator.
+//
+// A CTA sums one piece (up to `rows` rows of one adapter) for 256 columns and
+// 64 ranks (blockIdx.z).  Adapters of one piece are stored at once; the pieces
+// of larger ones go to scratch, where k_ad_outer_join adds them in order, so
+// results do not depend on timing.  The pieces are found from the offsets on
+// the device (the host knows only T): blockIdx.x counts them, adapters without
+// rows have one that stores zeros, and CTAs behind the last leave.  Bound by
+// the read of z; two CTAs an SM, so that one's copies run under the other's
+// start and end.
+#pragma once
+#include "adapter_gemm.cuh"
+
+namespace moe {
+
+struct AdOuterProblem {
+    const uint16_t *parts;  // [T][kAdParts][rp]
+    const uint16_t *z;      // [T x D]
+    float *g;               // [n x r x D]; nullptr: no such problem
+    int D;
+};
+struct AdOuterArgs {
+    AdOuterProblem pr[2];
+    int dch0;                // column blocks of problem 0
+    const int32_t *offsets;  // [n + 1] rows grouped by adapter
+    const int32_t *row;      // [offsets[n]]
+    float *partial;          // pieces of adapters with several
+    int rows;                // rows of one piece
+    int T, r, n;
+    int *status;
+};
+
+constexpr int kAOCols = 256, kAORanks = 64;  // of a CTA
+constexpr int kAORows = 32;                  // of a stage
+constexpr int kAOStages = 3;
+constexpr int kAOWarps = 8;                  // producers, then epilogue; one more issues the MMAs
+constexpr int kAOThreads = (kAOWarps + 1) * 32;
+constexpr int kAOBlock = kAORows * 128;      // 64 values of every row
+constexpr int kAOStage = (kAdParts + kAOCols / 64) * kAOBlock;
+
+// Arrive on `bar` (one of its counted arrivals) when this thread's copies so
+// far have landed.
+MOE_DEVINL void cp_async_arrive(uint64_t *bar)
+{
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar))
+                 : "memory");
+}
+
+struct AOSync {
+    uint64_t full[kAOStages];   // every producer's copies of the stage have landed
+    uint64_t empty[kAOStages];  // the MMAs reading it have completed
+    uint64_t done;              // every MMA has completed
+    uint32_t tmem_base;
+    int abort;
+};
+
+inline size_t ao_smem_bytes() { return 1024 + (size_t)kAOStages * kAOStage + sizeof(AOSync); }
+
+__global__ void __launch_bounds__(kAOThreads, 2) k_ad_outer(AdOuterArgs p)
+{
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *ring = g_align1024(smem_raw);
+    AOSync &sy = *reinterpret_cast<AOSync *>(ring + (size_t)kAOStages * kAOStage);
+    __shared__ int s_item[6];  // adapter, first row, rows, pieces, first scratch piece, piece
+    __shared__ int s_scan[2 * (kAOWarps + 1)];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        for (int s = 0; s < kAOStages; ++s) {
+            mbar_init(&sy.full[s], kAOWarps * 32);
+            mbar_init(&sy.empty[s], 1);
+        }
+        mbar_init(&sy.done, 1);
+        sy.abort = 0;
+        s_item[0] = -1;
+        fence_mbar_init();
+    }
+    pdl_wait();
+    pdl_trigger();
+    __syncthreads();
+    const int which = (int)blockIdx.y >= p.dch0;
+    const AdOuterProblem pr = which ? p.pr[1] : p.pr[0];
+    const int c0 = (blockIdx.y - (which ? p.dch0 : 0)) * kAOCols, j0 = blockIdx.z * kAORanks;
+    const int rp = ad_rp(p.r);
+
+    // which piece: pieces before adapter e, and scratch pieces before it
+    {
+        int base = 0, sbase = 0;
+        for (int e0 = 0; e0 < p.n; e0 += kAOThreads) {
+            const int e = e0 + tid;
+            int first = 0, len = 0, np = 0;
+            if (e < p.n) {
+                first = __ldcg(&p.offsets[e]);
+                len = __ldcg(&p.offsets[e + 1]) - first;
+                np = len > p.rows ? (len + p.rows - 1) / p.rows : 1;
+            }
+            // scans of the pieces and of those that go through scratch
+            int v = np, s = np > 1 ? np : 0;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int a = __shfl_up_sync(0xffffffffu, v, o), b = __shfl_up_sync(0xffffffffu, s, o);
+                if (lane >= o) {
+                    v += a;
+                    s += b;
+                }
+            }
+            if (lane == 31) {
+                s_scan[warp] = v;
+                s_scan[kAOWarps + 1 + warp] = s;
+            }
+            __syncthreads();
+            int wv = 0, wsum = 0, tv = 0, ts = 0;
+            for (int w = 0; w <= kAOWarps; ++w) {
+                if (w < warp) {
+                    wv += s_scan[w];
+                    wsum += s_scan[kAOWarps + 1 + w];
+                }
+                tv += s_scan[w];
+                ts += s_scan[kAOWarps + 1 + w];
+            }
+            const int start = base + wv + v - np;
+            const int i = blockIdx.x;
+            if (e < p.n && i >= start && i < start + np) {
+                s_item[0] = e;
+                s_item[5] = i - start;
+                s_item[1] = first + s_item[5] * p.rows;
+                s_item[2] = min(p.rows, len - s_item[5] * p.rows);
+                s_item[3] = np;
+                s_item[4] = sbase + wsum + s - (np > 1 ? np : 0);
+            }
+            base += tv;
+            sbase += ts;
+            __syncthreads();
+            if (s_item[0] >= 0 || base > (int)blockIdx.x)
+                break;
+        }
+    }
+    const int a = s_item[0];
+    if (a < 0)
+        return;
+    const int first = s_item[1], len = s_item[2], pieces = s_item[3];
+    const size_t plane = (size_t)p.r * pr.D;
+    float *out = pr.g + (size_t)a * plane;
+    if (pieces > 1) {  // scratch pieces hold both problems, problem 0 first
+        const size_t plane0 = p.pr[0].g ? (size_t)p.r * p.pr[0].D : 0;
+        const size_t both = plane0 + (p.pr[1].g ? (size_t)p.r * p.pr[1].D : 0);
+        out = p.partial + (size_t)(s_item[4] + s_item[5]) * both + (which ? plane0 : 0);
+    }
+    const int ranks = min(kAORanks, p.r - j0), cols = min(kAOCols, pr.D - c0);
+    if (len <= 0) {  // no rows
+        for (int i = tid; i < ranks * (cols / 4); i += kAOThreads)
+            *reinterpret_cast<float4 *>(out + (size_t)(j0 + i / (cols / 4)) * pr.D + c0 +
+                                        i % (cols / 4) * 4) = make_float4(0.f, 0.f, 0.f, 0.f);
+        return;
+    }
+    if (warp == kAOWarps) {
+        tmem_alloc(&sy.tmem_base, kAOCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sy.tmem_base;
+    const int ns = (len + kAORows - 1) / kAORows;
+
+    if (warp == kAOWarps) {
+        // ------------------------------------------------------------ MMAs
+        if (lane == 0) {
+            // both operands along M and N; N in whole sixteens
+            const uint32_t idesc =
+                umma_idesc_bf16(128, (cols + 15) & ~15) | (1u << 15) | (1u << 16);
+            uint32_t acc = 0;
+            for (int s = 0; s < ns; ++s) {
+                const int b = s % kAOStages;
+                if (!mbar_wait(&sy.full[b], (s / kAOStages) & 1, p.status)) {
+                    sy.abort = 1;
+                    break;
+                }
+                // the copies are ordinary writes to the tensor core's proxy; fenced
+                // here, where no copy is in flight (the fence of a thread that
+                // has some waits for them, which took away the stages' overlap)
+                asm volatile("fence.proxy.async;" ::: "memory");
+                tc_fence_after();
+                const uint32_t at = smem_addr(ring + (size_t)b * kAOStage);
+                const int steps = (min(kAORows, len - s * kAORows) + 15) / 16;
+                for (int k = 0; k < steps; ++k) {
+                    const uint64_t zd =
+                        umma_desc_mn_sw128(at + kAdParts * kAOBlock + k * 2048, kAOBlock);
+#pragma unroll
+                    for (int h = 0; h < kAdParts; ++h) {
+                        umma_bf16(tmem, umma_desc_mn_sw128(at + h * kAOBlock + k * 2048, kAOBlock), zd,
+                                  idesc, acc);
+                        acc = 1;
+                    }
+                }
+                umma_commit(&sy.empty[b]);
+            }
+            umma_commit(&sy.done);
+            mbar_wait(&sy.done, 0, p.status);
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------ copies
+        // a warp's rows of a stage: warp, warp + 8, ...; lane: a vector of eight
+        // columns of z, and (the first ones) of a part's ranks
+        const uint32_t sm = smem_addr(ring);
+        const int nc = min(rp - j0, kAORanks) / 8;  // vectors of a part
+        const int part = lane / nc, ch = lane - part * nc;
+        const bool pl = part < kAdParts, zl = lane * 8 < cols;
+        const uint16_t *zp = pr.z + c0 + lane * 8;
+        const uint16_t *up = pr.parts + (pl ? (size_t)part * rp + j0 + ch * 8 : 0);
+        const uint32_t zo = kAdParts * kAOBlock + (lane >> 3) * kAOBlock;
+        constexpr int kMine = kAORows / kAOWarps;
+        auto ids = [&](int s) {  // lane i: the row of this warp's i-th
+            const int m = s * kAORows + warp + kAOWarps * lane;
+            return lane < kMine && m < len ? __ldg(&p.row[first + m]) : -1;
+        };
+        int next = ids(0);
+        for (int s = 0; s < ns; ++s) {
+            const int id = next;
+            next = s + 1 < ns ? ids(s + 1) : -1;
+            const int b = s % kAOStages;
+            int w = 1;
+            if (lane == 0)
+                w = mbar_wait(&sy.empty[b], ((s / kAOStages) & 1) ^ 1, p.status);
+            if (!__shfl_sync(0xffffffffu, w, 0)) {
+                sy.abort = 1;
+                break;
+            }
+            const uint32_t at = sm + b * kAOStage;
+#pragma unroll
+            for (int i = 0; i < kMine; ++i) {
+                const int t = __shfl_sync(0xffffffffu, id, i);
+                const bool live = (unsigned)t < (unsigned)p.T;
+                const int row = warp + kAOWarps * i;
+                // zeros for rows behind the piece: they are multiplied too
+                cp_async16(at + zo + row * 128 + (((lane & 7) ^ (row & 7)) << 4),
+                           live && zl ? zp + (size_t)t * pr.D : pr.z, live && zl);
+                if (pl)
+                    cp_async16(at + part * kAOBlock + row * 128 + ((ch ^ (row & 7)) << 4),
+                               live ? up + (size_t)t * kAdParts * rp : pr.parts, live);
+            }
+            cp_async_arrive(&sy.full[b]);
+        }
+        cp_async_wait<0>();
+        // ------------------------------------------------------------ epilogue
+        // lanes 0-63 of tensor memory are the ranks: warps 0, 4 and 1, 5
+        if ((warp & 3) < 2 && (warp & 3) * 32 < ranks) {
+            int w = 1;
+            if (lane == 0)
+                w = mbar_wait(&sy.done, 0, p.status);
+            if (__shfl_sync(0xffffffffu, w, 0) && !*(volatile int *)&sy.abort) {
+                tc_fence_after();
+                for (int c = warp >> 2; c * 32 < cols; c += 2) {
+                    float v[32];
+                    __syncwarp();
+                    tmem_ld32(tmem + ((uint32_t)((warp & 3) * 32) << 16) + c * 32, v);
+                    ag_quad_rows(v);
+                    ag_put<float>(out + (size_t)j0 * pr.D + c0, pr.D, c * 32, (warp & 3) * 32, lane,
+                                  ranks, cols, v);
+                }
+                tc_fence_before();
+            }
+        }
+    }
+    __syncthreads();
+    if (warp == kAOWarps) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kAOCols);
+    }
+}
+
+// The pieces of adapter blockIdx.y added in order: four values a thread, eight
+// pieces' loads in flight.
+__global__ void __launch_bounds__(256) k_ad_outer_join(AdOuterArgs p)
+{
+    __shared__ int s_before;
+    const int tid = threadIdx.x, a = blockIdx.y;
+    if (tid == 0)
+        s_before = 0;
+    __syncthreads();
+    pdl_wait();
+    pdl_trigger();
+    const int len = __ldcg(&p.offsets[a + 1]) - __ldcg(&p.offsets[a]);
+    if (len <= p.rows)
+        return;
+    const int pieces = (len + p.rows - 1) / p.rows;
+    // scratch pieces of the adapters before
+    int before = 0;
+    for (int e = tid; e < a; e += 256) {
+        const int l = __ldcg(&p.offsets[e + 1]) - __ldcg(&p.offsets[e]);
+        if (l > p.rows)
+            before += (l + p.rows - 1) / p.rows;
+    }
+    before = __reduce_add_sync(0xffffffffu, before);
+    if ((tid & 31) == 0 && before)
+        atomicAdd(&s_before, before);
+    __syncthreads();
+    const size_t plane0 = p.pr[0].g ? (size_t)p.r * p.pr[0].D : 0;
+    const size_t plane1 = p.pr[1].g ? (size_t)p.r * p.pr[1].D : 0, both = plane0 + plane1;
+    const size_t o = ((size_t)blockIdx.x * 256 + tid) * 4;
+    if (o >= both)
+        return;
+    const float *from = p.partial + (size_t)s_before * both + o;
+    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int k0 = 0; k0 < pieces; k0 += 8) {
+        float4 v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (k0 + k < pieces)
+                v[k] = __ldcg(reinterpret_cast<const float4 *>(from + (size_t)(k0 + k) * both));
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (k0 + k < pieces) {
+                s.x += v[k].x;
+                s.y += v[k].y;
+                s.z += v[k].z;
+                s.w += v[k].w;
+            }
+    }
+    float *to = o < plane0 ? p.pr[0].g + (size_t)a * plane0 + o
+                           : p.pr[1].g + (size_t)a * plane1 + (o - plane0);
+    *reinterpret_cast<float4 *>(to) = s;
+}
+
+}  // namespace moe

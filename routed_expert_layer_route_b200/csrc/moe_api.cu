@@ -13,6 +13,7 @@
 #include "../../include/moe_testing.h"
 #include "adapter.cuh"
 #include "adapter_gemm.cuh"
+#include "adapter_outer.cuh"
 #include "balance.cuh"
 #include "combine.cuh"
 #include "ctopk.cuh"
@@ -190,12 +191,13 @@ static int device_info(DevInfo *&out)
             cudaFuncSetAttribute(k_ad_rows<2, true>, dsm, AdRowsShape<2>::kBytes) != cudaSuccess ||
             cudaFuncSetAttribute(k_ad_rows<4, true>, dsm, AdRowsShape<4>::kBytes) != cudaSuccess ||
             cudaFuncSetAttribute(k_ad_rows<8, true>, dsm, AdRowsShape<8>::kBytes) != cudaSuccess ||
-            cudaFuncSetAttribute(k_ad_inner_big<2>, dsm, AdBigShape<2>::kBytes) != cudaSuccess ||
-            cudaFuncSetAttribute(k_ad_inner_big<4>, dsm, AdBigShape<4>::kBytes) != cudaSuccess ||
-            cudaFuncSetAttribute(k_ad_inner_big<8>, dsm, AdBigShape<8>::kBytes) != cudaSuccess ||
-            cudaFuncSetAttribute(k_ad_outer<1>, dsm, AdOuterSmem<1>::kBytes) != cudaSuccess ||
-            cudaFuncSetAttribute(k_ad_outer<2>, dsm, AdOuterSmem<2>::kBytes) != cudaSuccess ||
-            cudaFuncSetAttribute(k_ad_outer<4>, dsm, AdOuterSmem<4>::kBytes) != cudaSuccess)
+            cudaFuncSetAttribute(k_ad_inner_big<2, 32>, dsm, AdBigShape<2, 32>::kBytes) != cudaSuccess ||
+            cudaFuncSetAttribute(k_ad_inner_big<2, 64>, dsm, AdBigShape<2, 64>::kBytes) != cudaSuccess ||
+            cudaFuncSetAttribute(k_ad_inner_big<4, 32>, dsm, AdBigShape<4, 32>::kBytes) != cudaSuccess ||
+            cudaFuncSetAttribute(k_ad_inner_big<4, 64>, dsm, AdBigShape<4, 64>::kBytes) != cudaSuccess ||
+            cudaFuncSetAttribute(k_ad_inner_big<8, 32>, dsm, AdBigShape<8, 32>::kBytes) != cudaSuccess ||
+            cudaFuncSetAttribute(k_ad_inner_big<8, 64>, dsm, AdBigShape<8, 64>::kBytes) != cudaSuccess ||
+            cudaFuncSetAttribute(k_ad_outer, dsm, (int)ao_smem_bytes()) != cudaSuccess)
             return MOE_ERR_CUDA;
         di.ad_pairs = pair_occupancy(k_ad_gemm<256>, kAGThreads, ag_smem_bytes<256>(), di.num_sms);
         const int small = 96 * 1024;
@@ -1528,23 +1530,24 @@ namespace moe {
 constexpr int kAdMaxDim = 16384, kAdMaxN = 1024;
 
 struct AdLayout {
-    size_t parts, given, offsets, row, pos, hist, arrive, partial, total;
+    size_t parts, given, offsets, row, pos, hist, splits, partial, total;
 };
 
-static int ad_col_blocks(int D) { return (D + kAdOutCols - 1) / kAdOutCols; }
-// 16-rank tiles of an outer-product CTA, and its blocks of ranks
-static int ad_mt(int r) { return r <= 16 ? 1 : r <= 32 ? 2 : 4; }
-static int ad_rank_blocks(int r) { return (r + 16 * ad_mt(r) - 1) / (16 * ad_mt(r)); }
+static int ad_col_blocks(int D) { return (D + kAOCols - 1) / kAOCols; }
+static int ad_rank_blocks(int r) { return (r + kAORanks - 1) / kAORanks; }
+
+// The projection's work items where K is split: at most one for each CTA pair.
+constexpr int kAGMaxItems = 74;
 
 // Outer products: rows of one piece.  One adapter may hold all rows, so a
-// column block's rows are cut into enough pieces that the CTAs of one adapter
-// fill the device about twice; a piece has 64 rows at least.
-constexpr int kAdOutTarget = 2 * 148;
+// column block's rows are cut into enough pieces that one adapter's CTAs
+// nearly fill the device's 296 places; a piece has 64 rows at least.
+constexpr int kAdOutTarget = 256;
 
 static int ad_piece_rows(int T, int blocks)
 {
     const int pieces = (kAdOutTarget + blocks - 1) / blocks;
-    const int rows = ((T + pieces - 1) / pieces + kAdOutRows - 1) / kAdOutRows * kAdOutRows;
+    const int rows = ((T + pieces - 1) / pieces + kAORows - 1) / kAORows * kAORows;
     return rows < 64 ? 64 : rows;
 }
 
@@ -1560,14 +1563,14 @@ static AdLayout ad_layout(int T, int din, int dout, int r, int n)
     L.row = o;      o = align256(o + sizeof(int32_t) * rows);
     L.pos = o;      o = align256(o + sizeof(int32_t) * rows);
     L.hist = o;     o = align256(o + sizeof(int32_t) * (size_t)perm_chunks(T) * n);
-    L.arrive = o;
-    o = align256(o + sizeof(int32_t) * (size_t)n * (ad_col_blocks(din) + ad_col_blocks(dout)) *
-                         ad_rank_blocks(r));
+    L.splits = o;
+    if (T > kAdRows)
+        o = align256(o + sizeof(float) * (size_t)kAGMaxItems * kAGRows * kAGSplitCols);
     // scratch pieces: an adapter of len > rows has at most 2 len / rows, so all
     // have at most 2 T / rows -- T / 32, and twice the pieces ad_piece_rows
-    // aims at, where blocks x 128 x 64 values at most make one
+    // aims at, where blocks x 256 x 64 values at most make one
     const size_t few = sizeof(float) * (rows / 32) * both;
-    const size_t many = sizeof(float) * 2 * ((size_t)kAdOutTarget * kAdOutCols * 64 + both);
+    const size_t many = sizeof(float) * 2 * ((size_t)kAdOutTarget * kAOCols * kAORanks + both);
     L.partial = o;  o = align256(o + (few < many ? few : many));
     L.total = o;
     return L;
@@ -1594,29 +1597,48 @@ static int ad_check_ws(const void *ws, size_t ws_bytes, size_t need)
 // From here on 64-row tiles (k_ad_inner_big) use the device better than 16-row
 // ones split over K.
 constexpr int kAdBigRows = 2048;
+// From here on the forward call groups its rows first: about 5 us, against
+// a pass over a tile for each of its adapters where rows come interleaved.
+constexpr int kAdGroupRows = 4096;
 
-// Inner products (and, with conv or zero_n, CTAs behind them for those).
+// Inner products (and, with conv, CTAs behind them for that).
 static int enqueue_ad_inner(AdInnerArgs a, bool inner, cudaStream_t s)
 {
     const int rp = (a.r + 15) & ~15;
-    const int64_t vals = a.conv ? (int64_t)a.T * rp : a.zero_n;
-    int64_t extra = (vals + 2047) / 2048;
-    if (a.row && a.u_out && extra < 16)
-        extra = 16;
-    if (extra > 148)
-        extra = 148;
+    const int64_t vals = a.conv ? (int64_t)a.T * rp : 0;
+    int64_t extra = (vals / 8 + 255) / 256;  // a thread for eight ranks of a row
     const dim3 block(kAdWarps * 32), big(kAdBigWarps * 32);
     if (inner && a.T >= kAdBigRows) {
-        a.lists = 2;  // a tile in which two requests meet takes no longer than the others
-        a.inner_ctas = (a.T + 63) / 64 * a.lists;
-        const unsigned gx = (unsigned)(a.inner_ctas + extra);
+        a.zero_u = a.u_out != nullptr;
+        if (a.zero_u && extra < 16)
+            extra = 16;
+        if (extra > 148)
+            extra = 148;
+        // 64 rows to a tile where that still makes about a tile for each SM
+        const int R = a.T >= 64 * 120 ? 64 : 32;
+        const int tiles = (a.T + R - 1) / R;
+        // CTAs for a tile's second, third, ... adapter
+        a.lists = a.row ? 2 : 4;
+        a.inner_ctas = tiles * a.lists;
+        const unsigned gx = (unsigned)(a.inner_ctas + extra), gy = (unsigned)((rp + 63) / 64);
+#define MOE_AD_BIG(NT, R) \
+    return launch(k_ad_inner_big<NT, R>, dim3(gx, gy), big, AdBigShape<NT, R>::kBytes, s, kPdl, a)
+        if (R == 64) {
+            if (rp <= 16)
+                MOE_AD_BIG(2, 64);
+            if (rp <= 32)
+                MOE_AD_BIG(4, 64);
+            MOE_AD_BIG(8, 64);
+        }
         if (rp <= 16)
-            return launch(k_ad_inner_big<2>, dim3(gx, 1), big, AdBigShape<2>::kBytes, s, kPdl, a);
+            MOE_AD_BIG(2, 32);
         if (rp <= 32)
-            return launch(k_ad_inner_big<4>, dim3(gx, 1), big, AdBigShape<4>::kBytes, s, kPdl, a);
-        return launch(k_ad_inner_big<8>, dim3(gx, (rp + 63) / 64), big, AdBigShape<8>::kBytes, s,
-                      kPdl, a);
+            MOE_AD_BIG(4, 32);
+        MOE_AD_BIG(8, 32);
+#undef MOE_AD_BIG
     }
+    if (extra > 148)
+        extra = 148;
     const int tiles = (a.T + 15) / 16;
     // CTAs that share a tile's adapters: 16 where the tiles alone leave the
     // device empty, fewer as they fill it
@@ -1627,7 +1649,7 @@ static int enqueue_ad_inner(AdInnerArgs a, bool inner, cudaStream_t s)
         return MOE_OK;
     const unsigned gx = (unsigned)(a.inner_ctas + extra);
 #define MOE_AD_INNER(NT) \
-    return launch(k_ad_inner<1, NT>, dim3(gx, (rp + 8 * NT - 1) / (8 * NT)), block, 0, s, kPdl, a)
+    return launch(k_ad_inner<NT>, dim3(gx, (rp + 8 * NT - 1) / (8 * NT)), block, 0, s, kPdl, a)
     // ranks of a CTA: 16 while the rows are few and CTAs would idle, else up to 64
     if (rp <= 16 || a.T <= kAdRows)
         MOE_AD_INNER(2);
@@ -1700,12 +1722,34 @@ static int enqueue_ad_product(AdProductArgs a, cudaStream_t s, const AdOne *one 
                 (rc = bf16_tile_map(&tw, a.w, a.din, a.dout, bn / 2)) != MOE_OK))
         return rc;
     const int tiles = rows * ((a.dout + bn - 1) / bn);
-    const dim3 grid(2 * (tiles < di->ad_pairs ? tiles : di->ad_pairs));
+    // K split over idle pairs where the K blocks that it takes off a pair's way
+    // (about 250 ns each) outweigh the join: 3 us and the sums' way through L2
+    // (65 rows, 2048 to 2048: 16.7 -> 14.8 us; 4096 rows, 2048 to 128 would
+    // lose: 20.4 -> 24.3)
+    const int pairs = di->ad_pairs < kAGMaxItems ? di->ad_pairs : kAGMaxItems;
+    a.splits = 1;
+    if (a.w && !wide && 2 * tiles <= pairs) {
+        const int nkb = (a.din + kGBK - 1) / kGBK;
+        int sp = pairs / tiles;
+        if (sp > kAGMaxSplits)
+            sp = kAGMaxSplits;
+        const int64_t saved = 250 * (int64_t)(nkb - (nkb + sp - 1) / sp);
+        if (saved > 3000 + (int64_t)sp * a.T * a.dout * 8 / 3500) {
+            const int per = (nkb + sp - 1) / sp;
+            a.splits = (nkb + per - 1) / per;  // none empty
+        }
+    }
+    const int items = tiles * a.splits;
+    const dim3 grid(2 * (items < di->ad_pairs ? items : di->ad_pairs));
     if (wide)
         return launch(k_ad_gemm<256>, grid, dim3(kAGThreads), ag_smem_bytes<256>(), s,
                       kPdl | kPair, tx, tw, tb, a);
-    return launch(k_ad_gemm<128>, grid, dim3(kAGThreads), ag_smem_bytes<128>(), s, kPdl | kPair, tx,
-                  tw, tb, a);
+    rc = launch(k_ad_gemm<128>, grid, dim3(kAGThreads), ag_smem_bytes<128>(), s, kPdl | kPair, tx, tw,
+                tb, a);
+    if (rc != MOE_OK || a.splits == 1)
+        return rc;
+    return launch(k_ad_join, dim3((unsigned)(((int64_t)a.T * (a.dout / 8) + 255) / 256)), dim3(256), 0,
+                  s, kPdl, a);
 }
 
 // Rows grouped by adapter (offsets, row): one CTA, or for large batches the
@@ -1731,15 +1775,14 @@ static bool ad_one_launch(int T, int dout, int r)
 
 static int enqueue_ad_outer(AdOuterArgs a, cudaStream_t s)
 {
-    const int mt = ad_mt(a.r), rb = ad_rank_blocks(a.r);
     a.dch0 = a.pr[0].g ? ad_col_blocks(a.pr[0].D) : 0;
     const int cols = a.dch0 + (a.pr[1].g ? ad_col_blocks(a.pr[1].D) : 0);
-    const dim3 grid(a.T / a.rows + a.n, cols, rb), block(256);
-    if (mt == 1)
-        return launch(k_ad_outer<1>, grid, block, AdOuterSmem<1>::kBytes, s, kPdl, a);
-    if (mt == 2)
-        return launch(k_ad_outer<2>, grid, block, AdOuterSmem<2>::kBytes, s, kPdl, a);
-    return launch(k_ad_outer<4>, grid, block, AdOuterSmem<4>::kBytes, s, kPdl, a);
+    const dim3 grid(a.T / a.rows + a.n, cols, ad_rank_blocks(a.r)), block(256);
+    const int rc = launch(k_ad_outer, grid, dim3(kAOThreads), ao_smem_bytes(), s, kPdl, a);
+    if (rc != MOE_OK || a.T <= a.rows)  // no adapter has two pieces
+        return rc;
+    const int64_t both = (int64_t)a.r * ((a.pr[0].g ? a.pr[0].D : 0) + (a.pr[1].g ? a.pr[1].D : 0));
+    return launch(k_ad_outer_join, dim3((unsigned)((both + 1023) / 1024), a.n), block, 0, s, kPdl, a);
 }
 
 }  // namespace moe
@@ -1790,12 +1833,13 @@ int moe_adapter_linear(const void *x_bf16, const void *w_bf16, const float *bias
     ai.status = &hdr->status;
     AdProductArgs ap = {x, static_cast<const uint16_t *>(w_bf16), bias,
                         static_cast<const uint16_t *>(lora_b_bf16), adapter, ai.parts, y,
-                        y_dtype == MOE_DTYPE_BF16, T, din, dout, r, n, hdr};
+                        y_dtype == MOE_DTYPE_BF16, T, din, dout, r, n, 1, at<float>(ws, L.splits),
+                        hdr};
     if (ad_one_launch(T, dout, r)) {
         const AdOne one = {ai.a, scale, u_out};
         return enqueue_ad_product(ap, s, &one);
     }
-    if (T >= kAdBigRows && n > 1) {  // tiles of few adapters, however the rows come
+    if (T > kAdGroupRows && n > 1) {  // tiles of few adapters, however the rows come
         if ((rc = enqueue_ad_group(adapter, T, n, ws, L, s)) != MOE_OK)
             return rc;
         ai.row = at<int32_t>(ws, L.row);
@@ -1850,7 +1894,6 @@ int moe_adapter_backward(const void *dy_bf16, const void *x_bf16, const void *w_
         if (rc != MOE_OK)
             return rc;
     }
-    const int cols = (d_lora_a ? ad_col_blocks(din) : 0) + (d_lora_b ? ad_col_blocks(dout) : 0);
     AdInnerArgs ai = {};
     ai.x = dy;
     ai.a = static_cast<const uint16_t *>(lora_b_bf16);
@@ -1859,8 +1902,6 @@ int moe_adapter_backward(const void *dy_bf16, const void *x_bf16, const void *w_
     ai.parts = at<uint16_t>(ws, L.parts);
     ai.conv = d_lora_b ? u : nullptr;
     ai.conv_parts = at<uint16_t>(ws, L.given);
-    ai.zero = at<int>(ws, L.arrive);
-    ai.zero_n = outer ? n * cols * ad_rank_blocks(r) : 0;
     ai.T = T;
     ai.din = dout;
     ai.r = r;
@@ -1875,7 +1916,8 @@ int moe_adapter_backward(const void *dy_bf16, const void *x_bf16, const void *w_
     if (dx) {
         AdProductArgs ap = {dy, static_cast<const uint16_t *>(w_t_bf16), nullptr,
                             static_cast<const uint16_t *>(lora_a_bf16), adapter, ai.parts, dx,
-                            dx_dtype == MOE_DTYPE_BF16, T, dout, din, r, n, hdr};
+                            dx_dtype == MOE_DTYPE_BF16, T, dout, din, r, n, 1,
+                            at<float>(ws, L.splits), hdr};
         if ((rc = enqueue_ad_product(ap, s)) != MOE_OK)
             return rc;
     }
@@ -1887,7 +1929,6 @@ int moe_adapter_backward(const void *dy_bf16, const void *x_bf16, const void *w_
     ao.offsets = offsets;
     ao.row = row;
     ao.partial = at<float>(ws, L.partial);
-    ao.arrive = ai.zero;
     // the same pieces whichever outputs are asked for, so that they do not change the sums
     ao.rows = ad_piece_rows(T, (ad_col_blocks(din) + ad_col_blocks(dout)) * ad_rank_blocks(r));
     ao.T = T;
