@@ -107,6 +107,99 @@ MOE_DEVINL uint4 ad_chunk(const uint16_t *row, int k, int K, bool live)
 }
 
 // ---------------------------------------------------------------------------
+// Rows grouped by adapter, in order inside a group (rows without one left
+// out): one CTA of W warps, each warp a run of at most 32 IDS rows that its
+// lanes hold, its counts of every adapter in shared memory of its own; then
+// the counts' prefix over adapters and warps gives each warp its places.
+// sg: ad_group_smem_bytes, zeroed here.
+struct AdGroupArgs {
+    const int32_t *adapter;  // [T]
+    int32_t *offsets;        // [n + 1]
+    int32_t *row;            // [offsets[n]]
+    int T, n;
+    int *status;
+};
+
+inline size_t ad_group_smem_bytes(int n, int warps) { return sizeof(int) * (size_t)n * (warps + 2); }
+
+template <int W, int IDS>
+MOE_DEVINL void ad_group(const AdGroupArgs &p, int *sg, int tid)
+{
+    __shared__ int scan[40];
+    const int warp = tid >> 5, lane = tid & 31;
+    int *start = sg + p.n * (W + 1);
+    const int run = ((p.T + W - 1) / W + 31) & ~31;
+    const int t0 = warp * run + lane;
+    int id[IDS];  // every row of the run at once
+    unsigned same[IDS];
+#pragma unroll
+    for (int i = 0; i < IDS; ++i)
+        id[i] = 32 * i < run && t0 + 32 * i < p.T ? __ldg(&p.adapter[t0 + 32 * i]) : MOE_EMPTY_SLOT;
+    for (int i = tid; i < p.n * (W + 1); i += W * 32)
+        sg[i] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < IDS; ++i) {
+        if (32 * i >= run)
+            break;
+        if ((unsigned)id[i] >= (unsigned)p.n) {
+            if (id[i] != MOE_EMPTY_SLOT)
+                set_status(p.status, MOE_ERR_DEVICE_CHECK);
+            id[i] = -1;
+        }
+        same[i] = __match_any_sync(0xffffffffu, id[i]);
+        if (id[i] >= 0 && (int)__ffs(same[i]) - 1 == lane)
+            sg[id[i] * (W + 1) + warp] += __popc(same[i]);
+        __syncwarp();
+    }
+    __syncthreads();
+    // per adapter: exclusive prefix over the warps and the total
+    for (int a = tid; a < p.n; a += W * 32) {
+        int sum = 0;
+        for (int w = 0; w < W; ++w) {
+            const int c = sg[a * (W + 1) + w];
+            sg[a * (W + 1) + w] = sum;
+            sum += c;
+        }
+        start[a] = sum;
+    }
+    __syncthreads();
+    const int total = block_exclusive_scan(start, p.n, scan);
+    for (int a = tid; a < p.n; a += W * 32)
+        p.offsets[a] = start[a];
+    if (tid == 0)
+        p.offsets[p.n] = total;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < IDS; ++i) {
+        if (32 * i >= run)
+            break;
+        const int a = id[i];
+        int base = 0;
+        if (a >= 0)
+            base = start[a] + sg[a * (W + 1) + warp];
+        __syncwarp();
+        if (a >= 0) {
+            p.row[base + __popc(same[i] & ((1u << lane) - 1u))] = t0 + 32 * i;
+            if ((int)__ffs(same[i]) - 1 == lane)
+                sg[a * (W + 1) + warp] += __popc(same[i]);
+        }
+        __syncwarp();
+    }
+}
+
+constexpr int kAdGroupWarps = 32, kAdGroupIds = 16;
+constexpr int kAdGroupMaxN = 256, kAdGroupMaxT = kAdGroupWarps * 32 * kAdGroupIds;
+
+__global__ void __launch_bounds__(kAdGroupWarps * 32) k_ad_group(AdGroupArgs p)
+{
+    extern __shared__ int sg[];
+    pdl_wait();
+    pdl_trigger();
+    ad_group<kAdGroupWarps, kAdGroupIds>(p, sg, threadIdx.x);
+}
+
+// ---------------------------------------------------------------------------
 // Inner products: u[t][j] = s_a <x_t, A_a[j]>, 0 for rows without an adapter.
 struct AdInnerArgs {
     const uint16_t *x;       // [T x din]
@@ -123,10 +216,13 @@ struct AdInnerArgs {
     int zero_u;              // clear u_out in rows without an adapter (k_ad_inner_big)
     int lists;               // CTAs that share a row tile's adapters
     int inner_ctas;          // CTAs of the inner products; those behind them convert
+    int grouping;            // k_ad_inner: one more CTA (of blockIdx.y 0) groups the rows
+    AdGroupArgs group;
     int *status;
 };
 
-constexpr int kAdWarps = 8;  // warps, which split K
+constexpr int kAdWarps = 8;            // warps, which split K
+constexpr int kAdSmallGroupT = 2048;  // most rows that one of its CTAs groups
 
 MOE_DEVINL void ad_put_parts(uint16_t *parts, int rp, int t, int j, float v)
 {
@@ -142,7 +238,8 @@ MOE_DEVINL void ad_put_parts(uint16_t *parts, int rp, int t, int j, float v)
 MOE_DEVINL void ad_convert(const AdInnerArgs &p, int tid)
 {
     const int rp = ad_rp(p.r);
-    const int64_t step = (int64_t)(gridDim.x - p.inner_ctas) * gridDim.y * blockDim.x;
+    const int64_t step =
+        (int64_t)(gridDim.x - p.grouping - p.inner_ctas) * gridDim.y * blockDim.x;
     const int64_t first =
         ((int64_t)(blockIdx.x - p.inner_ctas) * gridDim.y + blockIdx.y) * blockDim.x + tid;
     // rows without an adapter
@@ -169,20 +266,15 @@ MOE_DEVINL void ad_convert(const AdInnerArgs &p, int tid)
     }
 }
 
-// A tile's R <= 64 rows (st, -1: none) with their adapters (sa), and the
-// distinct ones in order of appearance; all threads of the CTA, which gets
-// their count.  A warp finds its rows' first ones by a match; a second warp
-// then leaves out what the first has.
+// A tile's R <= 32 rows (st, -1: none) with their adapters (sa), and the
+// distinct ones in order of appearance, by a match in one warp; all threads of
+// the CTA, which gets their count.
 template <int R>
 MOE_DEVINL int ad_tile_list(const AdInnerArgs &p, int i0, int rows, int tid, int *sa, int *st,
                             int *list, int *count)
 {
-    const int lane = tid & 31;
-    int a = -1;
-    unsigned firsts = 0u;
-    bool first = false;
-    if (tid < (R + 31) / 32 * 32) {
-        int t = -1;
+    if (tid < 32) {
+        int t = -1, a = -1;
         if (tid < min(rows, R)) {
             t = p.row ? __ldcg(&p.row[i0 + tid]) : i0 + tid;
             if ((unsigned)t < (unsigned)p.T)
@@ -195,32 +287,14 @@ MOE_DEVINL int ad_tile_list(const AdInnerArgs &p, int i0, int rows, int tid, int
             sa[tid] = a;
         }
         const unsigned same = __match_any_sync(0xffffffffu, a);
-        first = a >= 0 && (int)__ffs(same) - 1 == lane;
-        firsts = __ballot_sync(0xffffffffu, first);
-        if (tid < 32) {
-            if (first)
-                list[__popc(firsts & ((1u << lane) - 1u))] = a;
-            if (lane == 0)
-                *count = __popc(firsts);
-        }
+        const bool first = a >= 0 && (int)__ffs(same) - 1 == tid;
+        const unsigned firsts = __ballot_sync(0xffffffffu, first);
+        if (first)
+            list[__popc(firsts & ((1u << tid) - 1u))] = a;
+        if (tid == 0)
+            *count = __popc(firsts);
     }
     __syncthreads();
-    if (R > 32) {
-        const int have = *count;
-        if (tid >= 32 && tid < 64) {
-            for (int i = 0; i < have; ++i)
-                first = first && list[i] != a;
-            firsts = __ballot_sync(0xffffffffu, first);
-        }
-        __syncthreads();
-        if (tid >= 32 && tid < 64) {
-            if (first)
-                list[have + __popc(firsts & ((1u << lane) - 1u))] = a;
-            if (lane == 0)
-                *count = have + __popc(firsts);
-        }
-        __syncthreads();
-    }
     return *count;
 }
 
@@ -246,6 +320,12 @@ __global__ void __launch_bounds__(kAdWarps * 32, NT >= 8 ? 1 : 2) k_ad_inner(AdI
     pdl_wait();
     pdl_trigger();
     if ((int)blockIdx.x >= p.inner_ctas) {
+        if (p.grouping && blockIdx.x == gridDim.x - 1) {
+            extern __shared__ int sg[];
+            if (blockIdx.y == 0)
+                ad_group<kAdWarps, kAdSmallGroupT / (kAdWarps * 32)>(p.group, sg, tid);
+            return;
+        }
         ad_convert(p, tid);
         return;
     }
@@ -337,28 +417,31 @@ __global__ void __launch_bounds__(kAdWarps * 32, NT >= 8 ? 1 : 2) k_ad_inner(AdI
     }
 }
 
-// The same for many rows (8 NT >= r of blockIdx.y): R = 32 or 64 rows a CTA
-// and every lists-th of their adapters, one after another.  x and A_a stream
+// The same for many rows (8 NT >= r of blockIdx.y): 32 rows a CTA and every
+// lists-th of their adapters, one after another.  x and A_a stream
 // through shared memory in stages of 128 values of K, four deep, by
 // asynchronous copies that gather the rows; a warp multiplies 16 rows with
 // half of the ranks over a part of a stage, all its fragments loaded before
 // the first product (a few warps hide little latency).  Bound by the read of
-// x (an adapter's matrix is read once for each R rows that have it).
+// x (an adapter's matrix is read once for each 32 rows that have it, from L2;
+// 64 rows would halve that but leave one CTA an SM: 43 against 33 us for 8192
+// rows of 4096, rank 32).
 constexpr int kAdBigWarps = 16;
 
-template <int NT, int R>
+template <int NT>
 struct AdBigShape {
-    static constexpr int kRows = R, kK = 128, kStages = 4;
+    static constexpr int kRows = 32, kK = 128, kStages = 4;
     static constexpr int kPitch = kK * 2 + 16;  // bytes; 16 over: rows on other banks
     static constexpr int kStage = (kRows + 8 * NT) * kPitch;
     static constexpr int kBytes = kStages * kStage;
     static constexpr int kRedPitch = 8 * NT + 1;  // the halves' sums, in the stages' place
 };
 
-template <int NT, int R>
+template <int NT>
 __global__ void __launch_bounds__(kAdBigWarps * 32) k_ad_inner_big(AdInnerArgs p)
 {
-    using S = AdBigShape<NT, R>;
+    using S = AdBigShape<NT>;
+    constexpr int R = S::kRows;
     extern __shared__ __align__(16) uint8_t ab_smem[];
     __shared__ int sa[S::kRows], st[S::kRows], s_list[S::kRows];
     __shared__ int s_count;
@@ -383,22 +466,18 @@ __global__ void __launch_bounds__(kAdBigWarps * 32) k_ad_inner_big(AdInnerArgs p
     constexpr int kMT = R / 16, kKG = kAdBigWarps / (2 * kMT);  // row tiles, parts of a stage
     constexpr int NH = NT / 2, KS = S::kK / 16 / kKG;           // instructions of N and of K
     const int mt = warp % kMT, nh = warp / kMT % 2, kh = warp / (2 * kMT);
-    // this thread's vectors of a stage: column ck of rows tid / 16, + 32 of x,
-    // then of the adapter; nullptr: zeros
-    constexpr int kXV = R / 32, kVec = kXV + (NT + 3) / 4;
+    // this thread's vectors of a stage: column ck of row tid / 16 of x, then of
+    // ranks tid / 16, + 32 of the adapter; nullptr: zeros
+    constexpr int kVec = 1 + (NT + 3) / 4;
     const int ck = (tid & 15) * 8, r0 = tid >> 4;
     const uint32_t to0 = sm + r0 * S::kPitch + ck * 2;
     const uint16_t *src[kVec];
-#pragma unroll
-    for (int v = 0; v < kXV; ++v) {
-        const int t = st[r0 + 32 * v];
-        src[v] = t >= 0 ? p.x + (size_t)t * p.din + ck : nullptr;
-    }
+    src[0] = st[r0] >= 0 ? p.x + (size_t)st[r0] * p.din + ck : nullptr;
     for (int l = part; l < count; l += p.lists) {
         const int a = s_list[l];
 #pragma unroll
-        for (int v = kXV; v < kVec; ++v) {
-            const int j = j0 + r0 + 32 * (v - kXV);
+        for (int v = 1; v < kVec; ++v) {
+            const int j = j0 + r0 + 32 * (v - 1);
             src[v] = j < p.r && j < j0 + 8 * NT ? p.a + ((size_t)a * p.r + j) * p.din + ck : nullptr;
         }
         auto issue = [&](int s) {
@@ -510,87 +589,6 @@ __global__ void __launch_bounds__(kAdBigWarps * 32) k_ad_inner_big(AdInnerArgs p
         }
     }
 }
-
-// ---------------------------------------------------------------------------
-// Rows grouped by adapter, in order inside a group (rows without one left
-// out): one CTA, each warp a run of rows, its counts of every adapter in
-// shared memory of its own; then the counts' prefix over adapters and warps
-// gives each warp its places.
-constexpr int kAdGroupWarps = 32;
-constexpr int kAdGroupMaxN = 256, kAdGroupMaxT = 16384;
-
-__global__ void __launch_bounds__(kAdGroupWarps * 32) k_ad_group(const int32_t *adapter, int T, int n,
-                                                                 int32_t *offsets, int32_t *row,
-                                                                 int *status)
-{
-    extern __shared__ int sg[];  // [n][warps + 1] counts, then [n] starts
-    __shared__ int scan[40];
-    int *start = sg + n * (kAdGroupWarps + 1);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    for (int i = tid; i < n * (kAdGroupWarps + 1); i += kAdGroupWarps * 32)
-        sg[i] = 0;
-    __syncthreads();
-    pdl_wait();
-    pdl_trigger();
-    const int run = ((T + kAdGroupWarps - 1) / kAdGroupWarps + 31) & ~31;
-    const int t0 = warp * run + lane;
-    constexpr int kIds = kAdGroupMaxT / (kAdGroupWarps * 32);
-    int id[kIds];  // every row of the run at once
-    unsigned same[kIds];
-#pragma unroll
-    for (int i = 0; i < kIds; ++i)
-        id[i] = 32 * i < run && t0 + 32 * i < T ? __ldg(&adapter[t0 + 32 * i]) : MOE_EMPTY_SLOT;
-#pragma unroll
-    for (int i = 0; i < kIds; ++i) {
-        if (32 * i >= run)
-            break;
-        if ((unsigned)id[i] >= (unsigned)n) {
-            if (id[i] != MOE_EMPTY_SLOT)
-                set_status(status, MOE_ERR_DEVICE_CHECK);
-            id[i] = -1;
-        }
-        same[i] = __match_any_sync(0xffffffffu, id[i]);
-        if (id[i] >= 0 && (int)__ffs(same[i]) - 1 == lane)
-            sg[id[i] * (kAdGroupWarps + 1) + warp] += __popc(same[i]);
-        __syncwarp();
-    }
-    __syncthreads();
-    // per adapter: exclusive prefix over the warps and the total
-    for (int a = tid; a < n; a += kAdGroupWarps * 32) {
-        int sum = 0;
-        for (int w = 0; w < kAdGroupWarps; ++w) {
-            const int c = sg[a * (kAdGroupWarps + 1) + w];
-            sg[a * (kAdGroupWarps + 1) + w] = sum;
-            sum += c;
-        }
-        start[a] = sum;
-    }
-    __syncthreads();
-    const int total = block_exclusive_scan(start, n, scan);
-    for (int a = tid; a < n; a += kAdGroupWarps * 32)
-        offsets[a] = start[a];
-    if (tid == 0)
-        offsets[n] = total;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kIds; ++i) {
-        if (32 * i >= run)
-            break;
-        const int a = id[i];
-        int base = 0;
-        if (a >= 0)
-            base = start[a] + sg[a * (kAdGroupWarps + 1) + warp];
-        __syncwarp();
-        if (a >= 0) {
-            row[base + __popc(same[i] & ((1u << lane) - 1u))] = t0 + 32 * i;
-            if ((int)__ffs(same[i]) - 1 == lane)
-                sg[a * (kAdGroupWarps + 1) + warp] += __popc(same[i]);
-        }
-        __syncwarp();
-    }
-}
-
-inline size_t ad_group_smem_bytes(int n) { return sizeof(int) * (size_t)n * (kAdGroupWarps + 2); }
 
 // ---------------------------------------------------------------------------
 // The projection: y = x W^T + bias + sum_j u[t][j] B_a[j].  w nullptr: y

@@ -298,6 +298,28 @@ __global__ void __launch_bounds__(kAGThreads, 1)
                 tc_fence_after();
                 const uint32_t dt = tmem + buf * BN;
                 uint32_t acc = 0;
+                bool more = it % splits == 0;  // adapters' units to come
+                auto unit = [&]() {
+                    const int b = ub % kAGUBufs;
+                    if (!mbar_wait_cluster(&sy.ufull[b], (ub / kAGUBufs) & 1, status)) {
+                        sy.abort = 1;
+                        return;
+                    }
+                    tc_fence_after();
+                    const int what = *(volatile int *)&sy.u_what[b];
+                    const uint32_t st = smem_addr(ubuf + (size_t)b * S::kUBuf);
+                    if (what & 1) {
+                        const uint64_t bd = umma_desc_mn_sw128(st + kAGTileA, 2048);
+#pragma unroll
+                        for (int k = 0; k < kAdParts; ++k) {
+                            umma_bf16_pair(dt, umma_desc_sw128(st + k * 32), bd, idesc_mn, acc);
+                            acc = 1;
+                        }
+                    }
+                    umma_commit_pair_both(&sy.uempty[b]);
+                    ++ub;
+                    more = !(what & 2);
+                };
                 for (int kb = kb0; kb < kb1; ++kb, ++g) {
                     const int s = g % S::kStages;
                     if (!mbar_wait_cluster(&sy.full[s], (g / S::kStages) & 1, status)) {
@@ -314,28 +336,10 @@ __global__ void __launch_bounds__(kAGThreads, 1)
                     }
                     umma_commit_pair_both(&sy.empty[s]);
                 }
-                while (it % splits == 0 && !ag_aborted(sy)) {
-                    const int b = ub % kAGUBufs;
-                    if (!mbar_wait_cluster(&sy.ufull[b], (ub / kAGUBufs) & 1, status)) {
-                        sy.abort = 1;
-                        break;
-                    }
-                    tc_fence_after();
-                    const int what = *(volatile int *)&sy.u_what[b];
-                    const uint32_t st = smem_addr(ubuf + (size_t)b * S::kUBuf);
-                    if (what & 1) {
-                        const uint64_t bd = umma_desc_mn_sw128(st + kAGTileA, 2048);
-#pragma unroll
-                        for (int k = 0; k < kAdParts; ++k) {
-                            umma_bf16_pair(dt, umma_desc_sw128(st + k * 32), bd, idesc_mn, acc);
-                            acc = 1;
-                        }
-                    }
-                    umma_commit_pair_both(&sy.uempty[b]);
-                    ++ub;
-                    if (what & 2)
-                        break;
-                }
+                // (units between the K blocks, at fixed places, cost 3 us more for
+                // 8192 rows of 4096 than they hid)
+                while (more && !ag_aborted(sy))
+                    unit();
                 if (ag_aborted(sy))
                     break;
                 umma_commit_pair_both(&sy.acc_full[buf]);
@@ -445,12 +449,12 @@ __global__ void __launch_bounds__(kAGThreads, 1)
                 for (int c = 0; c < 2 * kAdParts; ++c)
                     *reinterpret_cast<uint4 *>(st + ut * 128 + ((c ^ (ut & 7)) << 4)) =
                         a >= 0 && a == e ? own[c] : make_uint4(0u, 0u, 0u, 0u);
-                if (a >= 0 && a == e && j + 16 < rp)
-                    load_own(j + 16);
                 asm volatile("fence.proxy.async;" ::: "memory");
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive_cluster(cluster_addr(&sy.ufull[b], 0));
+                if (a >= 0 && a == e && j + 16 < rp)  // after the fence, which waits for loads
+                    load_own(j + 16);
                 ++ub;
                 ++u0;
             } while (u0 < units);

@@ -191,12 +191,9 @@ static int device_info(DevInfo *&out)
             cudaFuncSetAttribute(k_ad_rows<2, true>, dsm, AdRowsShape<2>::kBytes) != cudaSuccess ||
             cudaFuncSetAttribute(k_ad_rows<4, true>, dsm, AdRowsShape<4>::kBytes) != cudaSuccess ||
             cudaFuncSetAttribute(k_ad_rows<8, true>, dsm, AdRowsShape<8>::kBytes) != cudaSuccess ||
-            cudaFuncSetAttribute(k_ad_inner_big<2, 32>, dsm, AdBigShape<2, 32>::kBytes) != cudaSuccess ||
-            cudaFuncSetAttribute(k_ad_inner_big<2, 64>, dsm, AdBigShape<2, 64>::kBytes) != cudaSuccess ||
-            cudaFuncSetAttribute(k_ad_inner_big<4, 32>, dsm, AdBigShape<4, 32>::kBytes) != cudaSuccess ||
-            cudaFuncSetAttribute(k_ad_inner_big<4, 64>, dsm, AdBigShape<4, 64>::kBytes) != cudaSuccess ||
-            cudaFuncSetAttribute(k_ad_inner_big<8, 32>, dsm, AdBigShape<8, 32>::kBytes) != cudaSuccess ||
-            cudaFuncSetAttribute(k_ad_inner_big<8, 64>, dsm, AdBigShape<8, 64>::kBytes) != cudaSuccess ||
+            cudaFuncSetAttribute(k_ad_inner_big<2>, dsm, AdBigShape<2>::kBytes) != cudaSuccess ||
+            cudaFuncSetAttribute(k_ad_inner_big<4>, dsm, AdBigShape<4>::kBytes) != cudaSuccess ||
+            cudaFuncSetAttribute(k_ad_inner_big<8>, dsm, AdBigShape<8>::kBytes) != cudaSuccess ||
             cudaFuncSetAttribute(k_ad_outer, dsm, (int)ao_smem_bytes()) != cudaSuccess)
             return MOE_ERR_CUDA;
         di.ad_pairs = pair_occupancy(k_ad_gemm<256>, kAGThreads, ag_smem_bytes<256>(), di.num_sms);
@@ -1541,14 +1538,15 @@ constexpr int kAGMaxItems = 74;
 
 // Outer products: rows of one piece.  One adapter may hold all rows, so a
 // column block's rows are cut into enough pieces that one adapter's CTAs
-// nearly fill the device's 296 places; a piece has 64 rows at least.
+// nearly fill the device's 296 places; a piece has 128 rows at least (four
+// stages, about what the join of two costs).
 constexpr int kAdOutTarget = 256;
 
 static int ad_piece_rows(int T, int blocks)
 {
     const int pieces = (kAdOutTarget + blocks - 1) / blocks;
     const int rows = ((T + pieces - 1) / pieces + kAORows - 1) / kAORows * kAORows;
-    return rows < 64 ? 64 : rows;
+    return rows < 128 ? 128 : rows;
 }
 
 static AdLayout ad_layout(int T, int din, int dout, int r, int n)
@@ -1567,9 +1565,9 @@ static AdLayout ad_layout(int T, int din, int dout, int r, int n)
     if (T > kAdRows)
         o = align256(o + sizeof(float) * (size_t)kAGMaxItems * kAGRows * kAGSplitCols);
     // scratch pieces: an adapter of len > rows has at most 2 len / rows, so all
-    // have at most 2 T / rows -- T / 32, and twice the pieces ad_piece_rows
+    // have at most 2 T / rows -- T / 64, and twice the pieces ad_piece_rows
     // aims at, where blocks x 256 x 64 values at most make one
-    const size_t few = sizeof(float) * (rows / 32) * both;
+    const size_t few = sizeof(float) * (rows / 64) * both;
     const size_t many = sizeof(float) * 2 * ((size_t)kAdOutTarget * kAOCols * kAORanks + both);
     L.partial = o;  o = align256(o + (few < many ? few : many));
     L.total = o;
@@ -1594,7 +1592,7 @@ static int ad_check_ws(const void *ws, size_t ws_bytes, size_t need)
     return ws_bytes < need ? MOE_ERR_WORKSPACE_TOO_SMALL : MOE_OK;
 }
 
-// From here on 64-row tiles (k_ad_inner_big) use the device better than 16-row
+// From here on 32-row tiles (k_ad_inner_big) use the device better than 16-row
 // ones split over K.
 constexpr int kAdBigRows = 2048;
 // From here on the forward call groups its rows first: about 5 us, against
@@ -1614,27 +1612,18 @@ static int enqueue_ad_inner(AdInnerArgs a, bool inner, cudaStream_t s)
             extra = 16;
         if (extra > 148)
             extra = 148;
-        // 64 rows to a tile where that still makes about a tile for each SM
-        const int R = a.T >= 64 * 120 ? 64 : 32;
-        const int tiles = (a.T + R - 1) / R;
+        const int tiles = (a.T + 31) / 32;
         // CTAs for a tile's second, third, ... adapter
         a.lists = a.row ? 2 : 4;
         a.inner_ctas = tiles * a.lists;
         const unsigned gx = (unsigned)(a.inner_ctas + extra), gy = (unsigned)((rp + 63) / 64);
-#define MOE_AD_BIG(NT, R) \
-    return launch(k_ad_inner_big<NT, R>, dim3(gx, gy), big, AdBigShape<NT, R>::kBytes, s, kPdl, a)
-        if (R == 64) {
-            if (rp <= 16)
-                MOE_AD_BIG(2, 64);
-            if (rp <= 32)
-                MOE_AD_BIG(4, 64);
-            MOE_AD_BIG(8, 64);
-        }
+#define MOE_AD_BIG(NT) \
+    return launch(k_ad_inner_big<NT>, dim3(gx, gy), big, AdBigShape<NT>::kBytes, s, kPdl, a)
         if (rp <= 16)
-            MOE_AD_BIG(2, 32);
+            MOE_AD_BIG(2);
         if (rp <= 32)
-            MOE_AD_BIG(4, 32);
-        MOE_AD_BIG(8, 32);
+            MOE_AD_BIG(4);
+        MOE_AD_BIG(8);
 #undef MOE_AD_BIG
     }
     if (extra > 148)
@@ -1645,11 +1634,12 @@ static int enqueue_ad_inner(AdInnerArgs a, bool inner, cudaStream_t s)
     int lists = 2 * 148 / tiles;
     a.lists = lists < 1 ? 1 : lists > 16 ? 16 : lists;
     a.inner_ctas = inner ? tiles * a.lists : 0;
-    if (a.inner_ctas + extra == 0)
+    if (a.inner_ctas + extra + a.grouping == 0)
         return MOE_OK;
-    const unsigned gx = (unsigned)(a.inner_ctas + extra);
+    const unsigned gx = (unsigned)(a.inner_ctas + extra + a.grouping);
+    const size_t smem = a.grouping ? ad_group_smem_bytes(a.n, kAdWarps) : 0;
 #define MOE_AD_INNER(NT) \
-    return launch(k_ad_inner<NT>, dim3(gx, (rp + 8 * NT - 1) / (8 * NT)), block, 0, s, kPdl, a)
+    return launch(k_ad_inner<NT>, dim3(gx, (rp + 8 * NT - 1) / (8 * NT)), block, smem, s, kPdl, a)
     // ranks of a CTA: 16 while the rows are few and CTAs would idle, else up to 64
     if (rp <= 16 || a.T <= kAdRows)
         MOE_AD_INNER(2);
@@ -1712,6 +1702,9 @@ static int enqueue_ad_product(AdProductArgs a, cudaStream_t s, const AdOne *one 
     if (di->ad_pairs < 1)
         return MOE_ERR_CUDA;
     const int rows = (a.T + kAGRows - 1) / kAGRows;
+    // 256 outputs to a tile while every pair gets one: a narrower tile takes
+    // its adapters' operands in twice as often (8192 rows, 2048 to 2048, rank
+    // 64: 166 against 107 us with 128, though their last round is fuller)
     const bool wide = rows * ((a.dout + 255) / 256) >= di->ad_pairs;
     const int bn = wide ? 256 : 128;
     CUtensorMap tx, tw, tb;
@@ -1759,9 +1752,11 @@ static int enqueue_ad_group(const int32_t *adapter, int T, int n, void *ws, cons
 {
     int32_t *offsets = at<int32_t>(ws, L.offsets), *row = at<int32_t>(ws, L.row);
     int *status = &static_cast<WsHeader *>(ws)->status;
-    if (T <= kAdGroupMaxT && n <= kAdGroupMaxN)
-        return launch(k_ad_group, dim3(1), dim3(kAdGroupWarps * 32), ad_group_smem_bytes(n), s, kPdl,
-                      adapter, T, n, offsets, row, status);
+    if (T <= kAdGroupMaxT && n <= kAdGroupMaxN) {
+        const AdGroupArgs g = {adapter, offsets, row, T, n, status};
+        return launch(k_ad_group, dim3(1), dim3(kAdGroupWarps * 32),
+                      ad_group_smem_bytes(n, kAdGroupWarps), s, kPdl, g);
+    }
     const PermOut po = {offsets, row, at<int32_t>(ws, L.pos), nullptr, nullptr};
     return enqueue_perm_parallel(adapter, T, 1, n, at<int>(ws, L.hist), po, status, s);
 }
@@ -1889,11 +1884,11 @@ int moe_adapter_backward(const void *dy_bf16, const void *x_bf16, const void *w_
     const uint16_t *x = static_cast<const uint16_t *>(x_bf16);
     int32_t *offsets = at<int32_t>(ws, L.offsets), *row = at<int32_t>(ws, L.row);
     const bool outer = d_lora_a || d_lora_b;
-    if (outer) {
-        rc = enqueue_ad_group(adapter, T, n, ws, L, s);
-        if (rc != MOE_OK)
-            return rc;
-    }
+    // the rows grouped by adapter: for few rows by a CTA of the inner launch,
+    // else before it, whose tiles then have few adapters however the rows come
+    const bool small = T < kAdBigRows && T <= kAdSmallGroupT && n <= kAdGroupMaxN;
+    if (outer && !small && (rc = enqueue_ad_group(adapter, T, n, ws, L, s)) != MOE_OK)
+        return rc;
     AdInnerArgs ai = {};
     ai.x = dy;
     ai.a = static_cast<const uint16_t *>(lora_b_bf16);
@@ -1907,7 +1902,10 @@ int moe_adapter_backward(const void *dy_bf16, const void *x_bf16, const void *w_
     ai.r = r;
     ai.n = n;
     ai.status = &hdr->status;
-    if (outer) {  // the grouping is there: a tile then has few adapters, however the rows come
+    if (outer && small) {
+        ai.grouping = 1;
+        ai.group = {adapter, offsets, row, T, n, &hdr->status};
+    } else if (outer) {
         ai.row = row;
         ai.rows = offsets + n;
     }
