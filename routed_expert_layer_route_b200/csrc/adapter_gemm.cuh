@@ -46,22 +46,24 @@ constexpr int kAGRows = 256;    // rows of a pair's tile
 constexpr int kAGThreads = 448;
 constexpr int kAGWarpU = 10;    // first of the U warps
 constexpr int kAGEpiWarps = 8;
-constexpr int kAGUBufs = 3;     // U/B buffers, a unit of 16 ranks each
+constexpr int kAGUBufs = 4;     // buffers of U, a unit of 16 ranks each
+constexpr int kAGBBufs = 8;     // buffers of B: a unit's copy starts kAGUBufs units ahead
 constexpr int kAGTileA = 128 * kGBK * 2;  // 16 KB: a CTA's rows of one K block
 
 template <int BN>
 struct AGShape {
     static constexpr int kTileB = BN / 2 * kGBK * 2;     // a CTA's outputs of one K block
     static constexpr int kStage = kAGTileA + kTileB;
-    static constexpr int kStages = BN == 256 ? 5 : 6;
+    static constexpr int kStages = BN == 256 ? 4 : 6;
     static constexpr int kUnitB = BN / 2 * 16 * 2;       // a CTA's outputs of one unit
-    static constexpr int kUBuf = kAGTileA + kUnitB;
+    static constexpr int kUB = kAGUBufs * kAGTileA + kAGBBufs * kUnitB;
 };
 
 struct AGSync {
     uint64_t full[6];             // CTA 0: both CTAs' tiles of stage s landed
     uint64_t empty[6];            // each CTA: the MMAs reading stage s finished
-    uint64_t ufull[kAGUBufs];     // CTA 0: both CTAs' U warps and B copies are there
+    uint64_t ufull[kAGUBufs];     // CTA 0: both CTAs' U warps have written
+    uint64_t bfull[kAGBBufs];     // CTA 0: both CTAs' copies of B landed
     uint64_t uempty[kAGUBufs];    // each CTA: the MMAs reading the buffer finished
     uint64_t acc_full[2];         // each CTA: accumulator set b is complete
     uint64_t acc_empty[2];        // CTA 0: both epilogues have read set b
@@ -79,7 +81,7 @@ template <int BN>
 inline size_t ag_smem_bytes()
 {
     return 1024 + (size_t)AGShape<BN>::kStages * AGShape<BN>::kStage +
-           (size_t)kAGUBufs * AGShape<BN>::kUBuf + sizeof(AGSync);
+           AGShape<BN>::kUB + sizeof(AGSync);
 }
 
 // Operand whose rows run along N (N contiguous), 128-byte swizzle: blocks of
@@ -197,7 +199,8 @@ __global__ void __launch_bounds__(kAGThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = g_align1024(smem_raw);
     uint8_t *ubuf = ring + (size_t)S::kStages * S::kStage;
-    AGSync &sy = *reinterpret_cast<AGSync *>(ubuf + (size_t)kAGUBufs * S::kUBuf);
+    uint8_t *bbuf = ubuf + (size_t)kAGUBufs * kAGTileA;
+    AGSync &sy = *reinterpret_cast<AGSync *>(ubuf + S::kUB);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = cluster_rank(), peer = rank ^ 1u;
     const bool lead = rank == 0;
@@ -212,6 +215,8 @@ __global__ void __launch_bounds__(kAGThreads, 1)
             mbar_init(&sy.ufull[b], 8);  // four U warps of each CTA
             mbar_init(&sy.uempty[b], 1);
         }
+        for (int b = 0; b < kAGBBufs; ++b)
+            mbar_init(&sy.bfull[b], 1);
         for (int b = 0; b < 2; ++b) {
             mbar_init(&sy.acc_full[b], 1);
             mbar_init(&sy.acc_empty[b], 2 * kAGEpiWarps);
@@ -285,7 +290,7 @@ __global__ void __launch_bounds__(kAGThreads, 1)
         }
     } else if (warp == kGWarpMma) {
         if (lane == 0 && lead) {
-            uint32_t g = 0, ub = 0, itc = 0;
+            uint32_t g = 0, ub = 0, bu = 0, itc = 0;
             const uint32_t idesc = umma_idesc_bf16(kAGRows, BN);
             const uint32_t idesc_mn = idesc | (1u << 16);  // B along N
             for (int it = pair; it < items; it += pairs, ++itc) {
@@ -307,9 +312,17 @@ __global__ void __launch_bounds__(kAGThreads, 1)
                     }
                     tc_fence_after();
                     const int what = *(volatile int *)&sy.u_what[b];
-                    const uint32_t st = smem_addr(ubuf + (size_t)b * S::kUBuf);
+                    const uint32_t st = smem_addr(ubuf + (size_t)b * kAGTileA);
                     if (what & 1) {
-                        const uint64_t bd = umma_desc_mn_sw128(st + kAGTileA, 2048);
+                        const int bb = bu % kAGBBufs;
+                        if (!mbar_wait_cluster(&sy.bfull[bb], (bu / kAGBBufs) & 1, status)) {
+                            sy.abort = 1;
+                            return;
+                        }
+                        tc_fence_after();
+                        ++bu;
+                        const uint64_t bd =
+                            umma_desc_mn_sw128(smem_addr(bbuf + (size_t)bb * S::kUnitB), 2048);
 #pragma unroll
                         for (int k = 0; k < kAdParts; ++k) {
                             umma_bf16_pair(dt, umma_desc_sw128(st + k * 32), bd, idesc_mn, acc);
@@ -350,7 +363,7 @@ __global__ void __launch_bounds__(kAGThreads, 1)
     } else if (warp >= kAGWarpU) {
         // ------------------------------------------------------------ U and B
         const int rp = ad_rp(p.r);
-        uint32_t ub = 0;
+        uint32_t ub = 0, bu = 0;  // units and copies of B so far
         bool waited = false;
         for (int it = pair; it < items; it += pairs) {
             if (it % splits)
@@ -397,39 +410,49 @@ __global__ void __launch_bounds__(kAGThreads, 1)
             const int units = sy.count * nch;
             const int o0 = i % ncol * BN + (int)rank * (BN / 2);
             const uint16_t *urow = p.parts + (size_t)(a >= 0 ? t : 0) * kAdParts * rp;
-            // this row's next unit of u, loaded before its turn comes
-            uint4 own[2 * kAdParts] = {};
-            auto load_own = [&](int j) {
+            // this row's next two units of u, loaded before their turn comes
+            uint4 own[2][2 * kAdParts] = {};
+            auto load_own = [&](uint4(&to)[2 * kAdParts], int j) {
 #pragma unroll
                 for (int c = 0; c < 2 * kAdParts; ++c)
-                    own[c] = __ldcg(reinterpret_cast<const uint4 *>(urow + c / 2 * rp + j) + c % 2);
+                    to[c] = __ldcg(reinterpret_cast<const uint4 *>(urow + c / 2 * rp + j) + c % 2);
             };
-            // B of unit u (one thread), once its buffer is free
-            auto load_b = [&](int u, int b) {
-                const int e = sy.list[u / nch], j = u % nch * 16;
-                uint8_t *st = ubuf + (size_t)b * S::kUBuf;
-                const uint32_t fb = cluster_addr(&sy.ufull[b], 0);
+            // B of unit u (one thread).  Its buffer was unit u - kAGBBufs's, whose
+            // MMAs are complete once U's buffer of unit u - kAGBBufs + kAGUBufs
+            // has come back empty, so a unit's copy starts kAGUBufs units ahead
+            int bl = 0, bj = 0;  // the next copy's adapter in the list and its first rank
+            auto load_b = [&]() {
+                const int e = sy.list[bl], j = bj, bb = bu % kAGBBufs;
+                bj += 16;
+                if (bj >= rp) {
+                    bj = 0;
+                    ++bl;
+                }
+                uint8_t *st = bbuf + (size_t)bb * S::kUnitB;
+                const uint32_t fb = cluster_addr(&sy.bfull[bb], 0);
                 if (lead)
-                    mbar_expect_tx(&sy.ufull[b], 2 * S::kUnitB);
+                    mbar_arrive_expect_tx(&sy.bfull[bb], 2 * S::kUnitB);
                 for (int c = 0; c < BN / 128; ++c)
-                    tma_load_3d_pair(st + kAGTileA + c * 2048, &tm_b, o0 + 64 * c, j, e, fb);
+                    tma_load_3d_pair(st + c * 2048, &tm_b, o0 + 64 * c, j, e, fb);
+                ++bu;
             };
-            int ahead = 0;  // units whose B is on its way already: the first buffers' before the wait
+            if (ut == 0)
+                for (int u = 0; u < min(units, kAGUBufs); ++u)
+                    load_b();
             if (!waited) {
-                ahead = min(units, kAGUBufs);
-                if (ut == 0)
-                    for (int u = 0; u < ahead; ++u)
-                        load_b(u, u);
                 pdl_wait();
                 pdl_trigger();
                 waited = true;
             }
-            if (a >= 0)
-                load_own(0);
-            int u0 = 0;
+            if (a >= 0) {
+                load_own(own[0], 0);
+                if (rp > 16)
+                    load_own(own[1], 16);
+            }
+            int u0 = 0, li = 0, j = 0;  // the unit: its adapter in the list, its first rank
             do {
                 const int b = ub % kAGUBufs;
-                const int e = u0 < units ? sy.list[u0 / nch] : -1, j = u0 % nch * 16;
+                const int e = u0 < units ? sy.list[li] : -1;
                 // one lane waits for its warp
                 int ok = 1;
                 if (lane == 0)
@@ -438,23 +461,31 @@ __global__ void __launch_bounds__(kAGThreads, 1)
                     sy.abort = 1;
                     break;
                 }
-                uint8_t *st = ubuf + (size_t)b * S::kUBuf;
-                if (ut == 0) {
-                    if (lead)
-                        sy.u_what[b] = (e >= 0 ? 1 : 0) | (u0 + 1 >= units ? 2 : 0);
-                    if (u0 >= ahead && e >= 0)
-                        load_b(u0, b);
-                }
+                uint8_t *st = ubuf + (size_t)b * kAGTileA;
+                if (ut == 0 && lead)
+                    sy.u_what[b] = (e >= 0 ? 1 : 0) | (u0 + 1 >= units ? 2 : 0);
 #pragma unroll
                 for (int c = 0; c < 2 * kAdParts; ++c)
                     *reinterpret_cast<uint4 *>(st + ut * 128 + ((c ^ (ut & 7)) << 4)) =
-                        a >= 0 && a == e ? own[c] : make_uint4(0u, 0u, 0u, 0u);
-                asm volatile("fence.proxy.async;" ::: "memory");
+                        a >= 0 && a == e ? own[0][c] : make_uint4(0u, 0u, 0u, 0u);
+                fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive_cluster(cluster_addr(&sy.ufull[b], 0));
-                if (a >= 0 && a == e && j + 16 < rp)  // after the fence, which waits for loads
-                    load_own(j + 16);
+                if (ut == 0 && u0 + kAGUBufs < units)
+                    load_b();
+                if (a >= 0 && a == e) {
+#pragma unroll
+                    for (int c = 0; c < 2 * kAdParts; ++c)
+                        own[0][c] = own[1][c];
+                    if (j + 32 < rp)  // after the fence, which waits for loads
+                        load_own(own[1], j + 32);
+                }
+                j += 16;
+                if (j >= rp) {
+                    j = 0;
+                    ++li;
+                }
                 ++ub;
                 ++u0;
             } while (u0 < units);

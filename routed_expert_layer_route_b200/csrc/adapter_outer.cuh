@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(kAOThreads, 2) k_ad_outer(AdOuterArgs p)
                 // the copies are ordinary writes to the tensor core's proxy; fenced
                 // here, where no copy is in flight (the fence of a thread that
                 // has some waits for them, which took away the stages' overlap)
-                asm volatile("fence.proxy.async;" ::: "memory");
+                fence_proxy_async_smem();
                 tc_fence_after();
                 const uint32_t at = smem_addr(ring + (size_t)b * kAOStage);
                 const int steps = (min(kAORows, len - s * kAORows) + 15) / 16;
