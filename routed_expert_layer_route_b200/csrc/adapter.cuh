@@ -603,6 +603,7 @@ struct AdProductArgs {
     void *y;                 // [T x dout]
     int y_bf16;
     int T, din, dout, r, n;
+    int segment;             // k_ad_gemm: most K blocks that one tensor-memory sum takes
     int splits;              // k_ad_gemm: parts of K; above 1 their sums go to partial
     float *partial;          // [tiles][splits][256 x kAGSplitCols]
     WsHeader *hdr;

@@ -24,6 +24,13 @@
 // SMs, where the last CTA to arrive alone would wait for its reads longer
 // than the split saves: 35 against 25 us for 4096 rows, 2048 to 128).
 //
+// The tensor cores cut their running sum to float32 at every step instead of
+// rounding it, so a float32 output's error grows with K (1.9e-6 of the 2-norm
+// at K = 2048, against 3.5e-7 for a float32 product). Float32 outputs
+// therefore take K in segments of kAGSegment blocks, each a sum of its own
+// that the epilogue adds up, rounded, in registers (BN = 128, whose two chunks
+// of a warp fit there); bf16 outputs need none of it.
+//
 // The two CTAs of a pair share tiles of 256 rows x BN outputs: each holds its
 // 128 rows of X and half of the outputs' rows of W in shared memory, and the
 // accumulators of its 128 rows (two sets of BN columns, so the epilogue of
@@ -43,6 +50,7 @@
 namespace moe {
 
 constexpr int kAGRows = 256;    // rows of a pair's tile
+constexpr int kAGSegment = 12;  // K blocks (768 values) of a float32 output's partial sum
 constexpr int kAGThreads = 448;
 constexpr int kAGWarpU = 10;    // first of the U warps
 constexpr int kAGEpiWarps = 8;
@@ -293,69 +301,74 @@ __global__ void __launch_bounds__(kAGThreads, 1)
             uint32_t g = 0, ub = 0, bu = 0, itc = 0;
             const uint32_t idesc = umma_idesc_bf16(kAGRows, BN);
             const uint32_t idesc_mn = idesc | (1u << 16);  // B along N
-            for (int it = pair; it < items; it += pairs, ++itc) {
-                const int buf = itc & 1;
+            for (int it = pair; it < items && !ag_aborted(sy); it += pairs) {
                 const int kb0 = it % splits * nks, kb1 = min(nkb, kb0 + nks);
-                if (!mbar_wait_cluster(&sy.acc_empty[buf], ((itc >> 1) & 1) ^ 1, status)) {
-                    sy.abort = 1;
-                    break;
-                }
-                tc_fence_after();
-                const uint32_t dt = tmem + buf * BN;
-                uint32_t acc = 0;
-                bool more = it % splits == 0;  // adapters' units to come
-                auto unit = [&]() {
-                    const int b = ub % kAGUBufs;
-                    if (!mbar_wait_cluster(&sy.ufull[b], (ub / kAGUBufs) & 1, status)) {
-                        sy.abort = 1;
-                        return;
-                    }
-                    tc_fence_after();
-                    const int what = *(volatile int *)&sy.u_what[b];
-                    const uint32_t st = smem_addr(ubuf + (size_t)b * kAGTileA);
-                    if (what & 1) {
-                        const int bb = bu % kAGBBufs;
-                        if (!mbar_wait_cluster(&sy.bfull[bb], (bu / kAGBBufs) & 1, status)) {
-                            sy.abort = 1;
-                            return;
-                        }
-                        tc_fence_after();
-                        ++bu;
-                        const uint64_t bd =
-                            umma_desc_mn_sw128(smem_addr(bbuf + (size_t)bb * S::kUnitB), 2048);
-#pragma unroll
-                        for (int k = 0; k < kAdParts; ++k) {
-                            umma_bf16_pair(dt, umma_desc_sw128(st + k * 32), bd, idesc_mn, acc);
-                            acc = 1;
-                        }
-                    }
-                    umma_commit_pair_both(&sy.uempty[b]);
-                    ++ub;
-                    more = !(what & 2);
-                };
-                for (int kb = kb0; kb < kb1; ++kb, ++g) {
-                    const int s = g % S::kStages;
-                    if (!mbar_wait_cluster(&sy.full[s], (g / S::kStages) & 1, status)) {
+                const int nseg = max(1, (kb1 - kb0 + p.segment - 1) / p.segment);
+                for (int sg = 0; sg < nseg; ++sg, ++itc) {
+                    const int buf = itc & 1;
+                    const int kbs = kb0 + sg * p.segment, kbe = min(kb1, kbs + p.segment);
+                    if (!mbar_wait_cluster(&sy.acc_empty[buf], ((itc >> 1) & 1) ^ 1, status)) {
                         sy.abort = 1;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t st = smem_addr(ring + (size_t)s * S::kStage);
+                    const uint32_t dt = tmem + buf * BN;
+                    uint32_t acc = 0;
+                    // adapters' units to come, with the last segment of the first split
+                    bool more = it % splits == 0 && sg == nseg - 1;
+                    auto unit = [&]() {
+                        const int b = ub % kAGUBufs;
+                        if (!mbar_wait_cluster(&sy.ufull[b], (ub / kAGUBufs) & 1, status)) {
+                            sy.abort = 1;
+                            return;
+                        }
+                        tc_fence_after();
+                        const int what = *(volatile int *)&sy.u_what[b];
+                        const uint32_t st = smem_addr(ubuf + (size_t)b * kAGTileA);
+                        if (what & 1) {
+                            const int bb = bu % kAGBBufs;
+                            if (!mbar_wait_cluster(&sy.bfull[bb], (bu / kAGBBufs) & 1, status)) {
+                                sy.abort = 1;
+                                return;
+                            }
+                            tc_fence_after();
+                            ++bu;
+                            const uint64_t bd =
+                                umma_desc_mn_sw128(smem_addr(bbuf + (size_t)bb * S::kUnitB), 2048);
 #pragma unroll
-                    for (int kk = 0; kk < kGBK / 16; ++kk) {
-                        umma_bf16_pair(dt, umma_desc_sw128(st + kk * 32),
-                                       umma_desc_sw128(st + kAGTileA + kk * 32), idesc, acc);
-                        acc = 1;
+                            for (int k = 0; k < kAdParts; ++k) {
+                                umma_bf16_pair(dt, umma_desc_sw128(st + k * 32), bd, idesc_mn, acc);
+                                acc = 1;
+                            }
+                        }
+                        umma_commit_pair_both(&sy.uempty[b]);
+                        ++ub;
+                        more = !(what & 2);
+                    };
+                    for (int kb = kbs; kb < kbe; ++kb, ++g) {
+                        const int s = g % S::kStages;
+                        if (!mbar_wait_cluster(&sy.full[s], (g / S::kStages) & 1, status)) {
+                            sy.abort = 1;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint32_t st = smem_addr(ring + (size_t)s * S::kStage);
+#pragma unroll
+                        for (int kk = 0; kk < kGBK / 16; ++kk) {
+                            umma_bf16_pair(dt, umma_desc_sw128(st + kk * 32),
+                                           umma_desc_sw128(st + kAGTileA + kk * 32), idesc, acc);
+                            acc = 1;
+                        }
+                        umma_commit_pair_both(&sy.empty[s]);
                     }
-                    umma_commit_pair_both(&sy.empty[s]);
+                    // (units between the K blocks, at fixed places, cost 3 us more for
+                    // 8192 rows of 4096 than they hid)
+                    while (more && !ag_aborted(sy))
+                        unit();
+                    if (ag_aborted(sy))
+                        break;
+                    umma_commit_pair_both(&sy.acc_full[buf]);
                 }
-                // (units between the K blocks, at fixed places, cost 3 us more for
-                // 8192 rows of 4096 than they hid)
-                while (more && !ag_aborted(sy))
-                    unit();
-                if (ag_aborted(sy))
-                    break;
-                umma_commit_pair_both(&sy.acc_full[buf]);
             }
             umma_commit_pair_both(&sy.drained);
             mbar_wait(&sy.drained, 0, status);
@@ -498,30 +511,76 @@ __global__ void __launch_bounds__(kAGThreads, 1)
         const int lq = warp & 3, eh = warp >= 6;
         const uint32_t lane_addr = tmem + ((uint32_t)(lq * 32) << 16);
         uint32_t itc = 0;
-        pdl_wait();
-        pdl_trigger();
         for (int it = pair; it < items; it += pairs, ++itc) {
-            const int buf = itc & 1, i = it / splits;
+            const int i = it / splits;
             const int row0 = i / ncol * kAGRows + (int)rank * 128;  // this CTA's first row
             const int t = row0 + lq * 32 + lane;
             const int o0 = i % ncol * BN;
-            int ok = 1;
-            if (lane == 0)
-                ok = mbar_wait_cluster(&sy.acc_full[buf], (itc >> 1) & 1, status);
-            if (!__shfl_sync(0xffffffffu, ok, 0)) {
-                sy.abort = 1;
-                break;
-            }
-            tc_fence_after();
             float *part = splits > 1 ? p.partial + ((size_t)it * 2 + rank) * 128 * BN : nullptr;
-#pragma unroll 1
-            for (int c = eh; c < BN / 32; c += 2) {
-                const int o = o0 + c * 32;
+            const int kb0 = it % splits * nks, kb1 = min(nkb, kb0 + nks);
+            const int nseg = max(1, (kb1 - kb0 + p.segment - 1) / p.segment);
+            auto wait_full = [&]() {
+                int ok = 1;
+                if (lane == 0)
+                    ok = mbar_wait_cluster(&sy.acc_full[itc & 1], (itc >> 1) & 1, status);
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+                if (!ok)
+                    sy.abort = 1;
+                tc_fence_after();
+                return ok != 0;
+            };
+            auto hand_back = [&]() {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive_cluster(cluster_addr(&sy.acc_empty[itc & 1], 0));
+            };
+            // the segments before the last, rounded sums (this warp's two chunks)
+            float sum[2][32];
+            if (BN == 128) {
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        sum[c][j] = 0.0f;
+                bool ok = true;
+                for (int sg = 0; sg < nseg - 1 && ok; ++sg) {
+                    ok = wait_full();
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        float v[32];
+                        __syncwarp();
+                        tmem_ld32(lane_addr + (itc & 1) * BN + (eh + 2 * c) * 32, v);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            sum[c][j] += v[j];
+                    }
+                    hand_back();
+                    ++itc;
+                }
+                if (!ok)
+                    break;
+            }
+            if (!wait_full())
+                break;
+            if (it == pair) {  // only the stores wait for the kernels before
+                pdl_wait();
+                pdl_trigger();
+            }
+            const int buf = itc & 1;
+#pragma unroll(BN == 128 ? 2 : 1)
+            for (int cc = 0; cc < BN / 64; ++cc) {
+                const int c = eh + 2 * cc, o = o0 + c * 32;
                 if (o >= p.dout)
                     break;
                 float v[32];
                 __syncwarp();
                 tmem_ld32(lane_addr + buf * BN + c * 32, v);
+                if (BN == 128) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        v[j] += sum[cc & 1][j];
+                }
                 if (splits > 1) {
                     ag_quad_rows(v);
                     ag_put<float>(part, BN, c * 32, lq * 32, lane, 128, BN, v);
@@ -591,10 +650,7 @@ __global__ void __launch_bounds__(kAGThreads, 1)
                                   v);
                 }
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive_cluster(cluster_addr(&sy.acc_empty[buf], 0));
+            hand_back();
         }
     }
     // tensor memory goes back once every MMA has completed, and neither CTA's

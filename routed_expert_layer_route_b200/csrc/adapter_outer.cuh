@@ -8,9 +8,12 @@
 // index contiguous): the gathered rows of z and of u's three bf16 parts go to
 // shared memory as they are, by asynchronous copies into the 128-byte swizzled
 // layout (blocks of 64 values x 8 rows), and tcgen05.mma reads them transposed.
-// Ranks are the M side (128 lanes of which up to 64 are ranks; the others read
-// the neighbouring block and are not looked at), 256 columns the N side; the
-// three parts of u add up in one accumulator.
+// Ranks are the M side, 256 columns the N side.  Of the 128 lanes the upper 64
+// take u's first part and the lower 64 the two smaller ones, in two
+// instructions a step: (first, second) and (a block of zeros, third).  The
+// tensor cores cut their running sum at every step instead of rounding it, so
+// the large sums get one step for 16 rows where all three parts in one would
+// take three; the epilogue adds the halves.
 //
 // A CTA sums one piece (up to `rows` rows of one adapter) for 256 columns and
 // 64 ranks (blockIdx.z).  Adapters of one piece are stored at once; the pieces
@@ -58,6 +61,8 @@ MOE_DEVINL void cp_async_arrive(uint64_t *bar)
                  : "memory");
 }
 
+constexpr int kAOHalfPitch = kAOCols + 4;  // floats of a lower-half row on its way to the upper
+
 struct AOSync {
     uint64_t full[kAOStages];   // every producer's copies of the stage have landed
     uint64_t empty[kAOStages];  // the MMAs reading it have completed
@@ -66,12 +71,14 @@ struct AOSync {
     int abort;
 };
 
-inline size_t ao_smem_bytes() { return 1024 + (size_t)kAOStages * kAOStage + sizeof(AOSync); }
+// the zeros, the stages (afterwards the lower half's sums), the barriers
+inline size_t ao_smem_bytes() { return 1024 + kAOBlock + (size_t)kAOStages * kAOStage + sizeof(AOSync); }
+static_assert(kAORanks * kAOHalfPitch * 4 <= kAOStages * kAOStage, "the lower half fits the stages");
 
 __global__ void __launch_bounds__(kAOThreads, 2) k_ad_outer(AdOuterArgs p)
 {
     extern __shared__ uint8_t smem_raw[];
-    uint8_t *ring = g_align1024(smem_raw);
+    uint8_t *zeros = g_align1024(smem_raw), *ring = zeros + kAOBlock;
     AOSync &sy = *reinterpret_cast<AOSync *>(ring + (size_t)kAOStages * kAOStage);
     __shared__ int s_item[6];  // adapter, first row, rows, pieces, first scratch piece, piece
     __shared__ int s_scan[2 * (kAOWarps + 1)];
@@ -86,6 +93,8 @@ __global__ void __launch_bounds__(kAOThreads, 2) k_ad_outer(AdOuterArgs p)
         s_item[0] = -1;
         fence_mbar_init();
     }
+    for (int i = tid; i < kAOBlock / 16; i += kAOThreads)
+        reinterpret_cast<uint4 *>(zeros)[i] = make_uint4(0u, 0u, 0u, 0u);
     pdl_wait();
     pdl_trigger();
     __syncthreads();
@@ -194,15 +203,16 @@ __global__ void __launch_bounds__(kAOThreads, 2) k_ad_outer(AdOuterArgs p)
                 tc_fence_after();
                 const uint32_t at = smem_addr(ring + (size_t)b * kAOStage);
                 const int steps = (min(kAORows, len - s * kAORows) + 15) / 16;
+                const uint32_t za = smem_addr(zeros);
                 for (int k = 0; k < steps; ++k) {
                     const uint64_t zd =
                         umma_desc_mn_sw128(at + kAdParts * kAOBlock + k * 2048, kAOBlock);
-#pragma unroll
-                    for (int h = 0; h < kAdParts; ++h) {
-                        umma_bf16(tmem, umma_desc_mn_sw128(at + h * kAOBlock + k * 2048, kAOBlock), zd,
-                                  idesc, acc);
-                        acc = 1;
-                    }
+                    // the parts' blocks lie one behind another; the zeros before
+                    // them all, the third part as far behind the zeros as it lies
+                    umma_bf16(tmem, umma_desc_mn_sw128(at + k * 2048, kAOBlock), zd, idesc, acc);
+                    umma_bf16(tmem,
+                              umma_desc_mn_sw128(za + k * 2048, at + 2 * kAOBlock - za), zd, idesc, 1);
+                    acc = 1;
                 }
                 umma_commit(&sy.empty[b]);
             }
@@ -255,24 +265,45 @@ __global__ void __launch_bounds__(kAOThreads, 2) k_ad_outer(AdOuterArgs p)
         }
         cp_async_wait<0>();
         // ------------------------------------------------------------ epilogue
-        // lanes 0-63 of tensor memory are the ranks: warps 0, 4 and 1, 5
-        if ((warp & 3) < 2 && (warp & 3) * 32 < ranks) {
-            int w = 1;
-            if (lane == 0)
-                w = mbar_wait(&sy.done, 0, p.status);
-            if (__shfl_sync(0xffffffffu, w, 0) && !*(volatile int *)&sy.abort) {
-                tc_fence_after();
-                for (int c = warp >> 2; c * 32 < cols; c += 2) {
-                    float v[32];
-                    __syncwarp();
-                    tmem_ld32(tmem + ((uint32_t)((warp & 3) * 32) << 16) + c * 32, v);
-                    ag_quad_rows(v);
-                    ag_put<float>(out + (size_t)j0 * pr.D + c0, pr.D, c * 32, (warp & 3) * 32, lane,
-                                  ranks, cols, v);
-                }
-                tc_fence_before();
+        // warps 2, 3, 6, 7 hold the lower half of tensor memory's lanes and hand
+        // their sums over; warps 0, 1, 4, 5 add them and store
+        int w = 1;
+        if (lane == 0)
+            w = mbar_wait(&sy.done, 0, p.status);
+        const bool good = __shfl_sync(0xffffffffu, w, 0) && !*(volatile int *)&sy.abort;
+        tc_fence_after();
+        const int quarter = warp & 3, r0 = (quarter & 1) * 32;  // first rank of this warp's lanes
+        const uint32_t from = tmem + ((uint32_t)(quarter * 32) << 16);
+        float *half = reinterpret_cast<float *>(ring);
+        if (good && quarter >= 2 && r0 < ranks)
+            for (int c = warp >> 2; c * 32 < cols; c += 2) {
+                float v[32];
+                __syncwarp();
+                tmem_ld32(from + c * 32, v);
+#pragma unroll
+                for (int j = 0; j < 32; j += 4)
+                    *reinterpret_cast<float4 *>(half + (r0 + lane) * kAOHalfPitch + c * 32 + j) =
+                        make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
             }
-        }
+        named_bar_sync(1, kAOWarps * 32);
+        if (good && quarter < 2 && r0 < ranks)
+            for (int c = warp >> 2; c * 32 < cols; c += 2) {
+                float v[32];
+                __syncwarp();
+                tmem_ld32(from + c * 32, v);
+#pragma unroll
+                for (int j = 0; j < 32; j += 4) {
+                    const float4 h = *reinterpret_cast<const float4 *>(
+                        half + (r0 + lane) * kAOHalfPitch + c * 32 + j);
+                    v[j] += h.x;
+                    v[j + 1] += h.y;
+                    v[j + 2] += h.z;
+                    v[j + 3] += h.w;
+                }
+                ag_quad_rows(v);
+                ag_put<float>(out + (size_t)j0 * pr.D + c0, pr.D, c * 32, r0, lane, ranks, cols, v);
+            }
+        tc_fence_before();
     }
     __syncthreads();
     if (warp == kAOWarps) {

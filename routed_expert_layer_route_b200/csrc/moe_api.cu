@@ -1533,6 +1533,18 @@ struct AdLayout {
 static int ad_col_blocks(int D) { return (D + kAOCols - 1) / kAOCols; }
 static int ad_rank_blocks(int r) { return (r + kAORanks - 1) / kAORanks; }
 
+// Whether k_ad_rows makes the projection: up to kAdFewRows rows always, up to
+// kAdRows while its CTAs, one for 16 outputs, read no more than 32 MB of x in
+// all (65 rows of 2048 to 2048 take 14.3 us on the tensor cores, 64 here 12.4; 64 of
+// 4096 to 4096: 39 against 32).  The layout has the tensor-core form's scratch
+// from kAdFewRows on.
+constexpr int kAdFewRows = 32;
+
+static bool ad_few_rows(int T, int din, int dout)
+{
+    return T <= kAdFewRows || (T <= kAdRows && (int64_t)T * din * dout <= (int64_t)1 << 28);
+}
+
 // The projection's work items where K is split: at most one for each CTA pair.
 constexpr int kAGMaxItems = 74;
 
@@ -1562,7 +1574,7 @@ static AdLayout ad_layout(int T, int din, int dout, int r, int n)
     L.pos = o;      o = align256(o + sizeof(int32_t) * rows);
     L.hist = o;     o = align256(o + sizeof(int32_t) * (size_t)perm_chunks(T) * n);
     L.splits = o;
-    if (T > kAdRows)
+    if (T > kAdFewRows)
         o = align256(o + sizeof(float) * (size_t)kAGMaxItems * kAGRows * kAGSplitCols);
     // scratch pieces: an adapter of len > rows has at most 2 len / rows, so all
     // have at most 2 T / rows -- T / 64, and twice the pieces ad_piece_rows
@@ -1669,7 +1681,7 @@ static int rank_tile_map(CUtensorMap *m, const void *base, uint64_t cols, uint64
 // one: the inner step's inputs where this launch does that step too
 static int enqueue_ad_product(AdProductArgs a, cudaStream_t s, const AdOne *one = nullptr)
 {
-    if (a.T <= kAdRows) {
+    if (ad_few_rows(a.T, a.din, a.dout)) {
         const dim3 block(kAdWarps * 32), grid((a.dout + 15) / 16);
         DevInfo *di;
         const int rc = device_info(di);
@@ -1702,10 +1714,14 @@ static int enqueue_ad_product(AdProductArgs a, cudaStream_t s, const AdOne *one 
     if (di->ad_pairs < 1)
         return MOE_ERR_CUDA;
     const int rows = (a.T + kAGRows - 1) / kAGRows;
+    // float32 outputs of a long K take it in segments
+    const int blocks = (a.din + kGBK - 1) / kGBK;
+    const bool segments = !a.y_bf16 && a.w && blocks > kAGSegment;
+    a.segment = segments ? kAGSegment : blocks + 1;
     // 256 outputs to a tile while every pair gets one: a narrower tile takes
     // its adapters' operands in twice as often (8192 rows, 2048 to 2048, rank
     // 64: 166 against 107 us with 128, though their last round is fuller)
-    const bool wide = rows * ((a.dout + 255) / 256) >= di->ad_pairs;
+    const bool wide = !segments && rows * ((a.dout + 255) / 256) >= di->ad_pairs;
     const int bn = wide ? 256 : 128;
     CUtensorMap tx, tw, tb;
     if ((rc = rank_tile_map(&tb, a.b, a.dout, a.r, a.n)) != MOE_OK)
@@ -1722,7 +1738,7 @@ static int enqueue_ad_product(AdProductArgs a, cudaStream_t s, const AdOne *one 
     const int pairs = di->ad_pairs < kAGMaxItems ? di->ad_pairs : kAGMaxItems;
     a.splits = 1;
     if (a.w && !wide && 2 * tiles <= pairs) {
-        const int nkb = (a.din + kGBK - 1) / kGBK;
+        const int nkb = blocks;
         int sp = pairs / tiles;
         if (sp > kAGMaxSplits)
             sp = kAGMaxSplits;
@@ -1828,7 +1844,7 @@ int moe_adapter_linear(const void *x_bf16, const void *w_bf16, const float *bias
     ai.status = &hdr->status;
     AdProductArgs ap = {x, static_cast<const uint16_t *>(w_bf16), bias,
                         static_cast<const uint16_t *>(lora_b_bf16), adapter, ai.parts, y,
-                        y_dtype == MOE_DTYPE_BF16, T, din, dout, r, n, 1, at<float>(ws, L.splits),
+                        y_dtype == MOE_DTYPE_BF16, T, din, dout, r, n, 0, 1, at<float>(ws, L.splits),
                         hdr};
     if (ad_one_launch(T, dout, r)) {
         const AdOne one = {ai.a, scale, u_out};
@@ -1914,7 +1930,7 @@ int moe_adapter_backward(const void *dy_bf16, const void *x_bf16, const void *w_
     if (dx) {
         AdProductArgs ap = {dy, static_cast<const uint16_t *>(w_t_bf16), nullptr,
                             static_cast<const uint16_t *>(lora_a_bf16), adapter, ai.parts, dx,
-                            dx_dtype == MOE_DTYPE_BF16, T, dout, din, r, n, 1,
+                            dx_dtype == MOE_DTYPE_BF16, T, dout, din, r, n, 0, 1,
                             at<float>(ws, L.splits), hdr};
         if ((rc = enqueue_ad_product(ap, s)) != MOE_OK)
             return rc;

@@ -20,6 +20,8 @@ SHAPES = [
     (255, 1000, 1544, 10, 3, "runs"), (257, 512, 520, 128, 40, "mixed"), (300, 64, 4096, 2, 300, "mixed"),
     (513, 2048, 128, 16, 4, "runs"), (1030, 1024, 776, 48, 6, "runs"), (700, 256, 128, 16, 2, "none"),
     (2561, 136, 2056, 24, 3, "runs"), (1200, 200, 4104, 16, 12, "mixed"),
+    (64, 4096, 2056, 16, 5, "mixed"), (40, 2056, 4096, 20, 6, "runs"), (4200, 64, 64, 4, 300, "mixed"),
+    (17000, 64, 72, 3, 5, "runs"), (2100, 136, 264, 100, 4, "mixed"), (2048, 1032, 128, 16, 1, "one"),
 ]
 
 
