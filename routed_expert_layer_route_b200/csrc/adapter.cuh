@@ -85,14 +85,6 @@ MOE_DEVINL void ldmatrix_x4(uint32_t addr, uint32_t (&r)[4])
                  : "r"(addr)
                  : "memory");
 }
-MOE_DEVINL void ldmatrix_x4_t(uint32_t addr, uint32_t (&r)[4])
-{
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
-}
-
 // Fragments straight from row-major memory: a thread (g = lane / 4,
 // q = lane % 4) loads the 16 bytes at K offset 32 c + 8 q of its row and feeds
 // them to two matrix instructions as elements (2q, 2q+1, 2q+8, 2q+9) of each.
@@ -418,14 +410,16 @@ __global__ void __launch_bounds__(kAdWarps * 32, NT >= 8 ? 1 : 2) k_ad_inner(AdI
 }
 
 // The same for many rows (8 NT >= r of blockIdx.y): 32 rows a CTA and every
-// lists-th of their adapters, one after another.  x and A_a stream
-// through shared memory in stages of 128 values of K, four deep, by
-// asynchronous copies that gather the rows; a warp multiplies 16 rows with
-// half of the ranks over a part of a stage, all its fragments loaded before
-// the first product (a few warps hide little latency).  Bound by the read of
-// x (an adapter's matrix is read once for each 32 rows that have it, from L2;
-// 64 rows would halve that but leave one CTA an SM: 43 against 33 us for 8192
-// rows of 4096, rank 32).
+// lists-th of their adapters, one after another.  x and A_a stream through
+// shared memory in stages of 128 values of K, four deep, by asynchronous
+// copies that gather the rows (one bulk copy a row and stage was slower: 95
+// against 33 us for 8192 rows of 4096, rank 32, the projection of 8 outputs
+// included); a warp multiplies 16 rows with half of the ranks over a part of a
+// stage, all its fragments loaded before the first product (a few warps hide
+// little latency).  Meant to be bound by the read of x, at about half of the
+// copy bandwidth so far; an adapter's matrix is read, from L2, once for each
+// 32 rows that have it (64 rows would halve that but leave one CTA an SM: 43
+// against 33 us for the same rows).
 constexpr int kAdBigWarps = 16;
 
 template <int NT>
@@ -650,7 +644,10 @@ struct AdOne {                    // what the one-launch form needs of the inner
 // its own wait, when every earlier kernel (which may have made x) is complete.
 // ONE: rows x ranks <= kAdOneRanks, one or a few rows; every CTA computes u
 // itself, a rank to a warp in turn, which reads the rows' adapters once for
-// each CTA (from L2) but saves a launch and its wait.
+// each CTA (from L2) but saves a launch and its wait (one row, 2048 to 128,
+// rank 16: 6.9 -> 5.2 us).
+// 32 rows, 2048 to 2048, rank 16, each row its own adapter: 8.5 us with the
+// inner launch, for 12.9 MB that have to be read (2.0 us).
 template <int NT>
 struct AdRowsShape {
     static constexpr int kDeep = NT <= 4 ? 8 : 4;              // chunks of a warp in a phase

@@ -24,12 +24,13 @@
 // SMs, where the last CTA to arrive alone would wait for its reads longer
 // than the split saves: 35 against 25 us for 4096 rows, 2048 to 128).
 //
-// The tensor cores cut their running sum to float32 at every step instead of
-// rounding it, so a float32 output's error grows with K (1.9e-6 of the 2-norm
-// at K = 2048, against 3.5e-7 for a float32 product). Float32 outputs
-// therefore take K in segments of kAGSegment blocks, each a sum of its own
-// that the epilogue adds up, rounded, in registers (BN = 128, whose two chunks
-// of a warp fit there); bf16 outputs need none of it.
+// The tensor cores' running float32 sum loses more at a step than a rounding:
+// an output's error grows with K (1.9e-6 of the 2-norm at K = 2048, against
+// 3.5e-7 for a float32 product).  Float32 outputs therefore take K in segments
+// of kAGSegment blocks, each a sum of its own that the epilogue adds up,
+// rounded, in registers (6.1e-7; BN = 128, whose two chunks of a warp fit
+// there; 1 to 2 us more for 4096 rows, 2048 to 128); bf16 outputs need none of
+// it.
 //
 // The two CTAs of a pair share tiles of 256 rows x BN outputs: each holds its
 // 128 rows of X and half of the outputs' rows of W in shared memory, and the
@@ -43,6 +44,14 @@
 // X and W need nothing of the inner kernel and are loaded while it runs (it
 // lets this kernel start after its own wait); the U warps and the epilogue
 // wait for it.  Every wait is bounded, as in gemm_pair.cuh.
+//
+// Bound by the matrix instructions for large tiles: 8192 rows, 4096 to 4096,
+// bf16: 187 us of the call's 226 in here, 1.47 PFLOP/s.  A K block of a tile
+// takes 0.36 to 0.38 us, a unit of adapters about 0.7 once the buffers that
+// were ready are used up (one way from "empty" to the products and back),
+// which is what many adapters in a tile cost: the same rows with every row
+// another request's take 386 us.  Small calls are bound by the chain of
+// launches, set-up and waits, 10 to 11 us for 100 rows.
 #pragma once
 #include "adapter.cuh"
 #include "gemm_pair.cuh"
@@ -111,14 +120,6 @@ MOE_DEVINL void tma_load_3d_pair(void *dst, const CUtensorMap *map, int x, int y
         : "memory");
 }
 
-// Bytes that the current phase of `bar` still waits for, without an arrival.
-MOE_DEVINL void mbar_expect_tx(uint64_t *bar, uint32_t bytes)
-{
-    asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(bar)),
-                 "r"(bytes)
-                 : "memory");
-}
-
 MOE_DEVINL void prefetch_tensormap(const CUtensorMap *m)
 {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
@@ -141,6 +142,15 @@ __device__ __noinline__ float ag_one(const AdProductArgs &p, int a, int t, int o
         }
     }
     return a >= 0 ? v + ad_part(p, a, t, o) : v;
+}
+
+// The NaNs among a row's 32 outputs from o on once more.
+__device__ __noinline__ void ag_again(const AdProductArgs &p, float *v, int t, int o)
+{
+    const int a = adapter_of(p.adapter, t, p.n, nullptr);
+    for (int j = 0; j < 32 && o + j < p.dout; ++j)
+        if (v[j] != v[j])
+            v[j] = ag_one(p, a, t, o + j);
 }
 
 MOE_DEVINL uint32_t ag_word(uint32_t w) { return w; }
@@ -561,12 +571,12 @@ __global__ void __launch_bounds__(kAGThreads, 1)
                 if (!ok)
                     break;
             }
-            if (!wait_full())
-                break;
             if (it == pair) {  // only the stores wait for the kernels before
                 pdl_wait();
                 pdl_trigger();
             }
+            if (!wait_full())
+                break;
             const int buf = itc & 1;
 #pragma unroll(BN == 128 ? 2 : 1)
             for (int cc = 0; cc < BN / 64; ++cc) {
@@ -591,11 +601,14 @@ __global__ void __launch_bounds__(kAGThreads, 1)
                 for (int j = 0; j < 32; ++j)
                     bad |= v[j] != v[j];
                 if (bad && t < p.T) {
-                    const int a = adapter_of(p.adapter, t, p.n, nullptr);
+                    float w[32];
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
-                        if (v[j] != v[j] && o + j < p.dout)
-                            v[j] = ag_one(p, a, t, o + j);
+                        w[j] = v[j];
+                    ag_again(p, w, t, o);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        v[j] = w[j];
                 }
                 if (p.bias) {
 #pragma unroll

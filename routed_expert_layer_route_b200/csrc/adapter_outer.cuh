@@ -11,18 +11,20 @@
 // Ranks are the M side, 256 columns the N side.  Of the 128 lanes the upper 64
 // take u's first part and the lower 64 the two smaller ones, in two
 // instructions a step: (first, second) and (a block of zeros, third).  The
-// tensor cores cut their running sum at every step instead of rounding it, so
-// the large sums get one step for 16 rows where all three parts in one would
-// take three; the epilogue adds the halves.
+// tensor cores' running sum loses more at a step than a rounding, so the large
+// sums get one step for 16 rows where all three parts in one would take three
+// (relative error at 8192 rows 8.6e-7 where that gave 1.3e-6; a float32
+// product 7.9e-7); the epilogue adds the halves.
 //
 // A CTA sums one piece (up to `rows` rows of one adapter) for 256 columns and
 // 64 ranks (blockIdx.z).  Adapters of one piece are stored at once; the pieces
 // of larger ones go to scratch, where k_ad_outer_join adds them in order, so
 // results do not depend on timing.  The pieces are found from the offsets on
 // the device (the host knows only T): blockIdx.x counts them, adapters without
-// rows have one that stores zeros, and CTAs behind the last leave.  Bound by
-// the read of z; two CTAs an SM, so that one's copies run under the other's
-// start and end.
+// rows have one that stores zeros, and CTAs behind the last leave.  Meant to be
+// bound by the read of z; two CTAs an SM, so that one's copies run under the
+// other's start and end.  Both gradients of 8192 rows, 2048 and 2048 columns,
+// rank 64, with their join: 37 us, 2 TB/s of z and the scratch pieces.
 #pragma once
 #include "adapter_gemm.cuh"
 

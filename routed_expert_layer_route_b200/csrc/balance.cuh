@@ -18,6 +18,11 @@
 //
 // Both kernels give a token one warp and hold its E logits in registers, so
 // each logit is read once; sums over a token are warp reductions in float32.
+// T = 65536, E = 512: k_balance 28 us, 4.9 TB/s, bound by the read (76% of the
+// copy bandwidth); k_route_backward with both parts, k1 = 5, k2 = 20, 90 us,
+// bound by its instructions (about 990 a row, half of them on the half-rate
+// comparison and logic pipe; reading and writing alone would take 32 us).
+// Small calls take 4 to 5 us, a launch and one pass of dependent loads.
 #pragma once
 #include "common.cuh"
 #include "grouped.cuh"

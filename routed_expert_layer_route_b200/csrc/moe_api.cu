@@ -189,8 +189,6 @@ static int device_info(DevInfo *&out)
             cudaFuncSetAttribute(k_ad_rows<8, false>, dsm, AdRowsShape<8>::kBytes) != cudaSuccess ||
             cudaFuncSetAttribute(k_ad_rows<1, true>, dsm, AdRowsShape<1>::kBytes) != cudaSuccess ||
             cudaFuncSetAttribute(k_ad_rows<2, true>, dsm, AdRowsShape<2>::kBytes) != cudaSuccess ||
-            cudaFuncSetAttribute(k_ad_rows<4, true>, dsm, AdRowsShape<4>::kBytes) != cudaSuccess ||
-            cudaFuncSetAttribute(k_ad_rows<8, true>, dsm, AdRowsShape<8>::kBytes) != cudaSuccess ||
             cudaFuncSetAttribute(k_ad_inner_big<2>, dsm, AdBigShape<2>::kBytes) != cudaSuccess ||
             cudaFuncSetAttribute(k_ad_inner_big<4>, dsm, AdBigShape<4>::kBytes) != cudaSuccess ||
             cudaFuncSetAttribute(k_ad_inner_big<8>, dsm, AdBigShape<8>::kBytes) != cudaSuccess ||
@@ -1692,12 +1690,8 @@ static int enqueue_ad_product(AdProductArgs a, cudaStream_t s, const AdOne *one 
     return launch(k_ad_rows<NT, ONE>, grid, block, AdRowsShape<NT>::kBytes, s, kPdl, a, o)
         if (one && a.T <= 8)
             MOE_AD_ROWS(1, true);
-        if (one && a.T <= 16)
+        if (one)  // 16 rows at most, of rank 1
             MOE_AD_ROWS(2, true);
-        if (one && a.T <= 32)
-            MOE_AD_ROWS(4, true);
-        if (one)
-            MOE_AD_ROWS(8, true);
         if (a.T <= 8)
             MOE_AD_ROWS(1, false);
         if (a.T <= 16)
@@ -1777,8 +1771,9 @@ static int enqueue_ad_group(const int32_t *adapter, int T, int n, void *ws, cons
     return enqueue_perm_parallel(adapter, T, 1, n, at<int>(ws, L.hist), po, status, s);
 }
 
-// The product's CTAs compute u themselves: a few row-ranks, and not so many
-// CTAs that reading the adapters in each costs more than the inner launch.
+// The product's CTAs compute u themselves: a few row-ranks (a warp takes two at
+// most), and not so many CTAs that reading the adapters in each costs more than
+// the inner launch.
 static bool ad_one_launch(int T, int dout, int r)
 {
     return T * r <= kAdOneRanks && (int64_t)T * r * dout <= 64 * 1024;
@@ -1961,7 +1956,7 @@ struct BalLayout {
     size_t p_acc, n_acc, arrive, z_part, total;
 };
 
-constexpr int kBalMaxGrid = 148 * 4;
+constexpr int kBalMaxGrid = 148 * 4;  // row_ctas at most on every SM
 
 static BalLayout bal_layout(int E)
 {
