@@ -208,7 +208,7 @@ struct AdInnerArgs {
     int zero_u;              // clear u_out in rows without an adapter (k_ad_inner_big)
     int lists;               // CTAs that share a row tile's adapters
     int inner_ctas;          // CTAs of the inner products; those behind them convert
-    int grouping;            // k_ad_inner: one more CTA (of blockIdx.y 0) groups the rows
+    int grouping;            // one more CTA (of blockIdx.y 0) groups the rows
     AdGroupArgs group;
     int *status;
 };
@@ -421,6 +421,7 @@ __global__ void __launch_bounds__(kAdWarps * 32, NT >= 8 ? 1 : 2) k_ad_inner(AdI
 // 32 rows that have it (64 rows would halve that but leave one CTA an SM: 43
 // against 33 us for the same rows).
 constexpr int kAdBigWarps = 16;
+constexpr int kAdBigGroupT = 4096;  // most rows that one of its CTAs groups
 
 template <int NT>
 struct AdBigShape {
@@ -444,6 +445,12 @@ __global__ void __launch_bounds__(kAdBigWarps * 32) k_ad_inner_big(AdInnerArgs p
     pdl_wait();
     pdl_trigger();
     if ((int)blockIdx.x >= p.inner_ctas) {
+        if (p.grouping && blockIdx.x == gridDim.x - 1) {
+            if (blockIdx.y == 0)
+                ad_group<kAdBigWarps, kAdBigGroupT / (kAdBigWarps * 32)>(
+                    p.group, reinterpret_cast<int *>(ab_smem), tid);
+            return;
+        }
         ad_convert(p, tid);
         return;
     }

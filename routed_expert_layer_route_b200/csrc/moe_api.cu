@@ -1616,7 +1616,7 @@ static int enqueue_ad_inner(AdInnerArgs a, bool inner, cudaStream_t s)
     const int64_t vals = a.conv ? (int64_t)a.T * rp : 0;
     int64_t extra = (vals / 8 + 255) / 256;  // a thread for eight ranks of a row
     const dim3 block(kAdWarps * 32), big(kAdBigWarps * 32);
-    if (inner && a.T >= kAdBigRows) {
+    if ((inner || a.grouping) && a.T >= kAdBigRows) {
         a.zero_u = a.u_out != nullptr;
         if (a.zero_u && extra < 16)
             extra = 16;
@@ -1625,8 +1625,9 @@ static int enqueue_ad_inner(AdInnerArgs a, bool inner, cudaStream_t s)
         const int tiles = (a.T + 31) / 32;
         // CTAs for a tile's second, third, ... adapter
         a.lists = a.row ? 2 : 4;
-        a.inner_ctas = tiles * a.lists;
-        const unsigned gx = (unsigned)(a.inner_ctas + extra), gy = (unsigned)((rp + 63) / 64);
+        a.inner_ctas = inner ? tiles * a.lists : 0;
+        const unsigned gx = (unsigned)(a.inner_ctas + extra + a.grouping);
+        const unsigned gy = (unsigned)((rp + 63) / 64);
 #define MOE_AD_BIG(NT) \
     return launch(k_ad_inner_big<NT>, dim3(gx, gy), big, AdBigShape<NT>::kBytes, s, kPdl, a)
         if (rp <= 16)
@@ -1895,9 +1896,11 @@ int moe_adapter_backward(const void *dy_bf16, const void *x_bf16, const void *w_
     const uint16_t *x = static_cast<const uint16_t *>(x_bf16);
     int32_t *offsets = at<int32_t>(ws, L.offsets), *row = at<int32_t>(ws, L.row);
     const bool outer = d_lora_a || d_lora_b;
-    // the rows grouped by adapter: for few rows by a CTA of the inner launch,
-    // else before it, whose tiles then have few adapters however the rows come
-    const bool small = T < kAdBigRows && T <= kAdSmallGroupT && n <= kAdGroupMaxN;
+    // the rows grouped by adapter: for few rows by a CTA of the inner launch
+    // (which saves about 5 us), else before it, whose tiles then have few
+    // adapters however the rows come
+    static_assert(kAdBigRows <= kAdSmallGroupT && kAdGroupRows <= kAdBigGroupT, "room to group");
+    const bool small = T <= kAdGroupRows && n <= kAdGroupMaxN;
     if (outer && !small && (rc = enqueue_ad_group(adapter, T, n, ws, L, s)) != MOE_OK)
         return rc;
     AdInnerArgs ai = {};

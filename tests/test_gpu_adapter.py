@@ -22,6 +22,7 @@ SHAPES = [
     (2561, 136, 2056, 24, 3, "runs"), (1200, 200, 4104, 16, 12, "mixed"),
     (64, 4096, 2056, 16, 5, "mixed"), (40, 2056, 4096, 20, 6, "runs"), (4200, 64, 64, 4, 300, "mixed"),
     (17000, 64, 72, 3, 5, "runs"), (2100, 136, 264, 100, 4, "mixed"), (2048, 1032, 128, 16, 1, "one"),
+    (2047, 72, 136, 9, 200, "mixed"), (4096, 264, 64, 12, 256, "mixed"), (4097, 64, 200, 33, 2, "runs"),
 ]
 
 
