@@ -23,6 +23,7 @@ SHAPES = [
     (64, 4096, 2056, 16, 5, "mixed"), (40, 2056, 4096, 20, 6, "runs"), (4200, 64, 64, 4, 300, "mixed"),
     (17000, 64, 72, 3, 5, "runs"), (2100, 136, 264, 100, 4, "mixed"), (2048, 1032, 128, 16, 1, "one"),
     (2047, 72, 136, 9, 200, "mixed"), (4096, 264, 64, 12, 256, "mixed"), (4097, 64, 200, 33, 2, "runs"),
+    (200, 8, 8, 3, 2, "mixed"), (2100, 8, 16, 20, 3, "mixed"), (66, 16384, 8, 1, 1, "one"), (12, 8, 16384, 16, 2, "mixed"),
 ]
 
 
@@ -283,6 +284,12 @@ def test_beside_the_routed_layer(T):
     moe.moe_adapter_linear(L.x, None, None, c.adapter, c.a, c.b, c.scale, y, c.workspace())
     want, e, _, _ = ref.linear(L.x, None, None, c.adapter, c.a, c.b, c.scale, product=product)
     ref.check(y, want, e)
+
+
+def test_pack_w_down_lays_an_adapter_out_by_rank():
+    c = ref.Case(20, 64, 128, 16, 3, seed=13)
+    torch_layout = c.b.transpose(1, 2).contiguous()  # [n x dout x r]
+    assert torch.equal(moe.moe_pack_w_down(torch_layout), c.b)
 
 
 def test_python_checks():
