@@ -19,8 +19,8 @@
 // Both kernels give a token one warp and hold its E logits in registers, so
 // each logit is read once; sums over a token are warp reductions in float32.
 // T = 65536, E = 512: k_balance 28 us, 4.9 TB/s, bound by the read (76% of the
-// copy bandwidth); k_route_backward with both parts, k1 = 5, k2 = 20, 90 us,
-// bound by its instructions (about 990 a row, half of them on the half-rate
+// copy bandwidth); k_route_backward with both parts, k1 = 5, k2 = 20, 87 us,
+// bound by its instructions (about 950 a row, 400 of them on the half-rate
 // comparison and logic pipe; reading and writing alone would take 32 us).
 // Small calls take 4 to 5 us, a launch and one pass of dependent loads.
 #pragma once
@@ -357,8 +357,8 @@ MOE_DEVINL float key_value(unsigned k)
 // The same border among a row's logits v themselves: true with thr where
 // exactly `want` of them (1 <= want < the row's length, largest m) are >= thr;
 // false where equal logits lie on the border.  The search first looks at each
-// lane's three largest only -- three votes a step instead of N comparisons --
-// which finds the border unless a lane holds four of the `want` largest; a
+// lane's three largest only -- three comparisons a step instead of N -- which
+// finds the border unless a lane holds four of the `want` largest; a
 // count over all elements says whether it did.
 template <int N>
 MOE_DEVINL bool border_value(const float (&v)[N], int want, float m, float &thr)
@@ -385,9 +385,8 @@ MOE_DEVINL bool border_value(const float (&v)[N], int want, float m, float &thr)
         while (h3 - l3 > 1u) {
             const unsigned mid = l3 + (h3 - l3) / 2u;
             const float x = key_value(mid);
-            const int n = __popc(__ballot_sync(0xffffffffu, a >= x)) +
-                          __popc(__ballot_sync(0xffffffffu, b >= x)) +
-                          __popc(__ballot_sync(0xffffffffu, c >= x));
+            // (one reduction: three votes' bit counts run at an eighth of the rate)
+            const int n = __reduce_add_sync(0xffffffffu, (int)(a >= x) + (int)(b >= x) + (int)(c >= x));
             if (n == want) {
                 thr = x;
                 int all = 0;
@@ -429,24 +428,34 @@ MOE_DEVINL bool border_value(const float (&v)[N], int want, float m, float &thr)
     return __reduce_add_sync(0xffffffffu, n) == want;
 }
 
-// N values of a row in shared memory (padded to whole vectors).
+// A lane's vector of a row in shared memory (padded to whole vectors).
+template <int VEC>
+MOE_DEVINL void smem_vec(const float *p, int E, int j, float (&v)[VEC])
+{
+    if (VEC == 4) {
+        float4 q = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (j < E)
+            q = *reinterpret_cast<const float4 *>(p + j);
+        v[0] = q.x;
+        v[1 % VEC] = q.y;
+        v[2 % VEC] = q.z;
+        v[3 % VEC] = q.w;
+    } else {
+        v[0] = j < E ? p[j] : 0.0f;
+    }
+}
+
+// All of a lane's values.
 template <int VEC, int N>
 MOE_DEVINL void smem_row(const float *p, int E, int lane, float (&v)[N])
 {
 #pragma unroll
     for (int i = 0; i < N; i += VEC) {
-        const int j = row_index<VEC>(i, lane);
-        if (VEC == 4) {
-            float4 q = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (j < E)
-                q = *reinterpret_cast<const float4 *>(p + j);
-            v[i] = q.x;
-            v[i + 1] = q.y;
-            v[i + 2] = q.z;
-            v[i + 3] = q.w;
-        } else {
-            v[i] = j < E ? p[j] : 0.0f;
-        }
+        float q[VEC];
+        smem_vec<VEC>(p, E, row_index<VEC>(i, lane), q);
+#pragma unroll
+        for (int k = 0; k < VEC; ++k)
+            v[i + k] = q[k];
     }
 }
 
@@ -651,15 +660,21 @@ __global__ void __launch_bounds__(kBalWarps * 32, row_ctas(N)) k_route_backward(
             const float ml = m * kLog2e;
             float s = 0.0f, fp = 0.0f, s2 = 0.0f;
             float gs = ge * (e >= 0 ? exp2_fast(fmaf(ze, kLog2e, -ml)) : 0.0f);
-            float f[N];
-            smem_row<VEC, N>(share, E, lane, f);
+            // the exponentials are kept (their unit has an eighth of the rate),
+            // f and g are read again
+            float x[N];
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const float x = exp2_fast(fmaf(v[i], kLog2e, -ml));
-                s += x;
-                fp = fmaf(f[i], x, fp);
-                if (v[i] >= thr)
-                    s2 += x;
+            for (int i = 0; i < N; i += VEC) {
+                float f[VEC];
+                smem_vec<VEC>(share, E, row_index<VEC>(i, lane), f);
+#pragma unroll
+                for (int k = 0; k < VEC; ++k) {
+                    x[i + k] = exp2_fast(fmaf(v[i + k], kLog2e, -ml));
+                    s += x[i + k];
+                    fp = fmaf(f[k], x[i + k], fp);
+                    if (v[i + k] >= thr)
+                        s2 += x[i + k];
+                }
             }
 #pragma unroll
             for (int o = 16; o >= 1; o >>= 1) {
@@ -672,15 +687,18 @@ __global__ void __launch_bounds__(kBalWarps * 32, row_ctas(N)) k_route_backward(
             gs *= inv2 * inv2;
             const float inv = 1.0f / s, q = per * inv;
             const float at = q * fmaf(-cb, fp * inv, 2.0f * a.c_z * (m + logf(s))), qf = q * cb;
-            float g[N];
-            smem_row<VEC, N>(gw, E, lane, g);
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const float x = exp2_fast(fmaf(v[i], kLog2e, -ml));
-                float k = fmaf(qf, f[i], at);
-                if (v[i] >= thr)
-                    k += fmaf(g[i], inv2, -gs);
-                v[i] = x * k;
+            for (int i = 0; i < N; i += VEC) {
+                float f[VEC], g[VEC];
+                smem_vec<VEC>(share, E, row_index<VEC>(i, lane), f);
+                smem_vec<VEC>(gw, E, row_index<VEC>(i, lane), g);
+#pragma unroll
+                for (int k = 0; k < VEC; ++k) {
+                    float c = fmaf(qf, f[k], at);
+                    if (v[i + k] >= thr)
+                        c += fmaf(g[k], inv2, -gs);
+                    v[i + k] = x[i + k] * c;
+                }
             }
             store_row<VEC, N>(a, t, lane, v);
         }
