@@ -63,14 +63,15 @@ MOE_DEVINL void load_row(const float *z, int E, int lane, float (&v)[N])
     }
 }
 
-// e^(z - m) as 2^(z log2 e - m log2 e): one fused multiply-add (whose rounding
-// of m log2 e is the same factor for the whole row and cancels in a softmax)
-// and the hardware's power of two (2^-22 relative).
+// e^(z - m): the difference first, so that the largest logit's is exactly 1 (a
+// fused multiply-add would leave a few last bits, which show where a weight of
+// 1 cancels: k2 = 1 has no gradient through its weight at all); then the
+// hardware's power of two (2^-22 relative).
 constexpr float kLog2e = 1.4426950408889634f;
-MOE_DEVINL float exp2_fast(float x)
+MOE_DEVINL float exp_from(float z, float m)
 {
     float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"((z - m) * kLog2e));
     return y;
 }
 
@@ -160,7 +161,7 @@ __global__ void __launch_bounds__(kBalWarps * 32, row_ctas(N)) k_balance(Balance
         float s = 0.0f;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            v[i] = exp2_fast(fmaf(v[i], kLog2e, -m * kLog2e));
+            v[i] = exp_from(v[i], m);
             s += v[i];
         }
         s = warp_sum(s);
@@ -525,15 +526,14 @@ __device__ __noinline__ void route_row_general(const RouteBackArgs &a, int t, in
                 key[i] = 0u;
         }
     }
-    const float ml = m * kLog2e, m2l = m2 * kLog2e;
     float g[N], f[N];
     smem_row<VEC, N>(gw, E, lane, g);
     smem_row<VEC, N>(share, E, lane, f);
     float s = 0.0f, fp = 0.0f, s2 = 0.0f, gs = 0.0f;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        const float x = exp2_fast(fmaf(v[i], kLog2e, -ml));
-        const float w = key[i] >= thr ? exp2_fast(fmaf(v[i], kLog2e, -m2l)) : 0.0f;
+        const float x = exp_from(v[i], m);
+        const float w = key[i] >= thr ? exp_from(v[i], m2) : 0.0f;
         s += x;
         fp = fmaf(f[i], x, fp);
         s2 += w;
@@ -550,8 +550,8 @@ __device__ __noinline__ void route_row_general(const RouteBackArgs &a, int t, in
     const float at = q * fmaf(-cb, fp / s, 2.0f * a.c_z * (m + logf(s))), qf = q * cb;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        const float x = exp2_fast(fmaf(v[i], kLog2e, -ml));
-        const float w = key[i] >= thr ? exp2_fast(fmaf(v[i], kLog2e, -m2l)) : 0.0f;
+        const float x = exp_from(v[i], m);
+        const float w = key[i] >= thr ? exp_from(v[i], m2) : 0.0f;
         v[i] = x * fmaf(qf, f[i], at);
         if (key[i] >= thr)
             v[i] = fmaf(w, inv2 * (g[i] - gs), v[i]);
@@ -657,9 +657,8 @@ __global__ void __launch_bounds__(kBalWarps * 32, row_ctas(N)) k_route_backward(
             route_row_general<VEC, N>(a, t, e, gw, share, lane, m, per, cb);
         } else {
             // dz = e^(z - m) (1/S2 (g - sum g w) in K2  +  per/S (cb (f - sum f p) + 2 c_z lse))
-            const float ml = m * kLog2e;
             float s = 0.0f, fp = 0.0f, s2 = 0.0f;
-            float gs = ge * (e >= 0 ? exp2_fast(fmaf(ze, kLog2e, -ml)) : 0.0f);
+            float gs = ge * (e >= 0 ? exp_from(ze, m) : 0.0f);
             // the exponentials are kept (their unit has an eighth of the rate),
             // f and g are read again
             float x[N];
@@ -669,7 +668,7 @@ __global__ void __launch_bounds__(kBalWarps * 32, row_ctas(N)) k_route_backward(
                 smem_vec<VEC>(share, E, row_index<VEC>(i, lane), f);
 #pragma unroll
                 for (int k = 0; k < VEC; ++k) {
-                    x[i + k] = exp2_fast(fmaf(v[i + k], kLog2e, -ml));
+                    x[i + k] = exp_from(v[i + k], m);
                     s += x[i + k];
                     fp = fmaf(f[k], x[i + k], fp);
                     if (v[i + k] >= thr)
@@ -684,7 +683,7 @@ __global__ void __launch_bounds__(kBalWarps * 32, row_ctas(N)) k_route_backward(
                 gs += __shfl_xor_sync(0xffffffffu, gs, o);
             }
             const float inv2 = s2 == 0.0f ? 0.0f : 1.0f / s2;  // 0: no weights asked for
-            gs *= inv2 * inv2;
+            gs *= inv2;
             const float inv = 1.0f / s, q = per * inv;
             const float at = q * fmaf(-cb, fp * inv, 2.0f * a.c_z * (m + logf(s))), qf = q * cb;
 #pragma unroll
@@ -696,7 +695,7 @@ __global__ void __launch_bounds__(kBalWarps * 32, row_ctas(N)) k_route_backward(
                 for (int k = 0; k < VEC; ++k) {
                     float c = fmaf(qf, f[k], at);
                     if (v[i + k] >= thr)
-                        c += fmaf(g[k], inv2, -gs);
+                        c = fmaf(g[k] - gs, inv2, c);
                     v[i + k] = x[i + k] * c;
                 }
             }

@@ -173,6 +173,20 @@ def test_balance_gradient_against_differences():
         assert abs(got - num) <= 1e-5 * float(dz.double().norm() * v.norm())
 
 
+@pytest.mark.parametrize("E,k1", [(8, 1), (300, 1), (64, 3)])
+def test_one_expert_in_k2_leaves_the_losses_alone(E, k1):
+    # a weight of 1 has no gradient, however small the losses' is beside it; nor
+    # have empty slots or a K2 of one given expert
+    T = 500
+    z, idx, _, d_w = make(T, E, k1, seed=16)
+    if k1 > 1:
+        idx[:, 1:] = ref.EMPTY
+    counts = balance(z, idx)[0]
+    kw = dict(counts=counts, balance_coef=1e-3, z_coef=1e-5)
+    both = route_backward(z, idx[:, :1].contiguous(), 1, d_w[:, :1].contiguous(), **kw)
+    assert torch.equal(both, route_backward(z, idx[:, :1].contiguous(), 1, None, **kw))
+
+
 def test_ties_take_the_lower_index():
     T, E, k1, k2 = 6, 96, 2, 7
     z = torch.zeros(T, E, device=DEV)
