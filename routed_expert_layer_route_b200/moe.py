@@ -413,12 +413,19 @@ _BYTE = (torch.bool, torch.uint8)
 
 
 def _given(where, device, *tensors):
-    """Each of (tensor or None, dtypes, shape) is dense, of one of these dtypes
-    and of this shape, on the current device; else MOE_ERR_INVALID_ARG."""
+    """The pointers (None for None) of (tensor or None, dtypes, shape): each
+    dense, of one of these dtypes and of this shape, on the current device;
+    else MOE_ERR_INVALID_ARG."""
+    pointers = []
     for t, dtypes, shape in tensors:
-        if t is not None and not (t.dtype in dtypes and t.shape == shape and t.is_contiguous()
-                                  and t.get_device() == device):
+        if t is None:
+            pointers.append(None)
+        elif (t.dtype in dtypes and t.shape == shape and t.is_contiguous()
+              and t.get_device() == device):
+            pointers.append(t.data_ptr())
+        else:
             raise MoeError(MOE_ERR_INVALID_ARG, where)
+    return pointers
 
 
 def _out_dtype(t):
@@ -446,14 +453,14 @@ def moe_adapter_linear(x, w, bias, adapter, lora_a, lora_b, scale, y, ws, u_out=
     w None: the adapters' part is added to y."""
     T, din = x.shape
     n, r, dout = lora_b.shape
-    _given("moe_adapter_linear", torch.cuda.current_device(), (x, _BF16, (T, din)),
-           (w, _BF16, (dout, din)), (bias, _F32, (dout,)), (adapter, _I32, (T,)),
-           (lora_a, _BF16, (n, r, din)), (lora_b, _BF16, (n, r, dout)), (scale, _F32, (n,)),
-           (y, _OUT, (T, dout)), (u_out, _F32, (T, r)))
+    *inputs, yp, up = _given(
+        "moe_adapter_linear", torch.cuda.current_device(), (x, _BF16, (T, din)),
+        (w, _BF16, (dout, din)), (bias, _F32, (dout,)), (adapter, _I32, (T,)),
+        (lora_a, _BF16, (n, r, din)), (lora_b, _BF16, (n, r, dout)), (scale, _F32, (n,)),
+        (y, _OUT, (T, dout)), (u_out, _F32, (T, r)))
     wsp, wsn = _ws_args(ws)
-    _check(lib().moe_adapter_linear(_p(x), _p(w), _p(bias), _p(adapter), _p(lora_a), _p(lora_b),
-                                    _p(scale), T, din, dout, r, n, _p(y), _out_dtype(y), _p(u_out),
-                                    wsp, wsn, _stream(stream)), "moe_adapter_linear")
+    _check(lib().moe_adapter_linear(*inputs, T, din, dout, r, n, yp, _out_dtype(y), up, wsp, wsn,
+                                    _stream(stream)), "moe_adapter_linear")
 
 
 def moe_adapter_backward(dy, x, w_t, adapter, lora_a, lora_b, scale, u, d_lora_a, d_lora_b, ws,
@@ -463,16 +470,15 @@ def moe_adapter_backward(dy, x, w_t, adapter, lora_a, lora_b, scale, u, d_lora_a
     u as moe_adapter_linear's u_out."""
     T, dout = dy.shape
     n, r, din = lora_a.shape
-    _given("moe_adapter_backward", torch.cuda.current_device(), (dy, _BF16, (T, dout)),
-           (x, _BF16, (T, din)), (w_t, _BF16, (din, dout)), (adapter, _I32, (T,)),
-           (lora_a, _BF16, (n, r, din)), (lora_b, _BF16, (n, r, dout)), (scale, _F32, (n,)),
-           (u, _F32, (T, r)), (d_lora_a, _F32, (n, r, din)), (d_lora_b, _F32, (n, r, dout)),
-           (dx, _OUT, (T, din)))
+    *inputs, dap, dbp, dxp = _given(
+        "moe_adapter_backward", torch.cuda.current_device(), (dy, _BF16, (T, dout)),
+        (x, _BF16, (T, din)), (w_t, _BF16, (din, dout)), (adapter, _I32, (T,)),
+        (lora_a, _BF16, (n, r, din)), (lora_b, _BF16, (n, r, dout)), (scale, _F32, (n,)),
+        (u, _F32, (T, r)), (d_lora_a, _F32, (n, r, din)), (d_lora_b, _F32, (n, r, dout)),
+        (dx, _OUT, (T, din)))
     wsp, wsn = _ws_args(ws)
-    _check(lib().moe_adapter_backward(_p(dy), _p(x), _p(w_t), _p(adapter), _p(lora_a), _p(lora_b),
-                                      _p(scale), _p(u), T, din, dout, r, n, _p(dx), _out_dtype(dx),
-                                      _p(d_lora_a), _p(d_lora_b), wsp, wsn, _stream(stream)),
-           "moe_adapter_backward")
+    _check(lib().moe_adapter_backward(*inputs, T, din, dout, r, n, dxp, _out_dtype(dx), dap, dbp, wsp,
+                                      wsn, _stream(stream)), "moe_adapter_backward")
 
 
 def moe_balance_workspace_size(T, E):
@@ -497,13 +503,13 @@ def moe_balance_loss(logits, topk_idx, balance_coef, z_coef, counts, loss, ws, t
     token_mask [T] bool or uint8, False for padding."""
     T, E = logits.shape
     k1 = topk_idx.shape[-1]
-    _given("moe_balance_loss", torch.cuda.current_device(), (logits, _F32, (T, E)),
-           (topk_idx, _I32, (T, k1)), (token_mask, _BYTE, (T,)), (counts, _I32, (E + 1,)),
-           (loss, _F32, (3,)), (prob_mean, _F32, (E,)))
+    *inputs, counts, loss, prob_mean = _given(
+        "moe_balance_loss", torch.cuda.current_device(), (logits, _F32, (T, E)),
+        (topk_idx, _I32, (T, k1)), (token_mask, _BYTE, (T,)), (counts, _I32, (E + 1,)),
+        (loss, _F32, (3,)), (prob_mean, _F32, (E,)))
     wsp, wsn = _ws_args(ws)
-    _check(lib().moe_balance_loss(_p(logits), _p(topk_idx), _p(token_mask), T, E, k1,
-                                  float(balance_coef), float(z_coef), _p(counts), _p(loss),
-                                  _p(prob_mean), wsp, wsn, _stream(stream)), "moe_balance_loss")
+    _check(lib().moe_balance_loss(*inputs, T, E, k1, float(balance_coef), float(z_coef), counts, loss,
+                                  prob_mean, wsp, wsn, _stream(stream)), "moe_balance_loss")
 
 
 def moe_route_backward(logits, topk_idx, k2, d_topk_w, dlogits, counts=None, balance_coef=0.0,
@@ -513,12 +519,13 @@ def moe_route_backward(logits, topk_idx, k2, d_topk_w, dlogits, counts=None, bal
     float32 scalar, None for 1)."""
     T, E = logits.shape
     k1 = topk_idx.shape[-1]
-    _given("moe_route_backward", torch.cuda.current_device(), (logits, _F32, (T, E)),
-           (topk_idx, _I32, (T, k1)), (d_topk_w, _F32, (T, k1)), (counts, _I32, (E + 1,)),
-           (token_mask, _BYTE, (T,)), (dlogits, _OUT, (T, E)),
-           (d_loss, _F32, d_loss.shape if d_loss is not None and d_loss.numel() == 1 else None))
+    *inputs, d_loss, dzp = _given(
+        "moe_route_backward", torch.cuda.current_device(), (logits, _F32, (T, E)),
+        (topk_idx, _I32, (T, k1)), (d_topk_w, _F32, (T, k1)), (counts, _I32, (E + 1,)),
+        (token_mask, _BYTE, (T,)),
+        (d_loss, _F32, d_loss.shape if d_loss is not None and d_loss.numel() == 1 else None),
+        (dlogits, _OUT, (T, E)))
     wsp, wsn = _ws_args(ws)
-    _check(lib().moe_route_backward(_p(logits), _p(topk_idx), _p(d_topk_w), _p(counts),
-                                    _p(token_mask), T, E, k1, k2, float(balance_coef),
-                                    float(z_coef), _p(d_loss), _p(dlogits), _out_dtype(dlogits),
-                                    wsp, wsn, _stream(stream)), "moe_route_backward")
+    _check(lib().moe_route_backward(*inputs, T, E, k1, k2, float(balance_coef), float(z_coef), d_loss,
+                                    dzp, _out_dtype(dlogits), wsp, wsn, _stream(stream)),
+           "moe_route_backward")
