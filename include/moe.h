@@ -413,7 +413,9 @@ int moe_adapter_backward(const void *dy_bf16, const void *x_bf16, const void *w_
  *   - counts [E + 1] from moe_balance_loss (or summed over several batches
  *     or ranks): the gradient of balance_coef L_bal + z_coef L_z, the counts
  *     held fixed, times d_loss (device float32 scalar, NULL: 1).
- *   k1 <= k2; k2 >= E: all experts.  ws (nullable) takes the status word. */
+ *   k1 <= k2; k2 >= E: all experts.  A row with a NaN or +inf logit has a
+ *   NaN gradient wherever that logit enters, in its own row only.  ws
+ *   (nullable) takes the status word. */
 size_t moe_balance_workspace_size(int T, int E);
 int moe_balance_loss(const float *logits, const int32_t *topk_idx, const unsigned char *token_mask,
                      int T, int E, int k1, float balance_coef, float z_coef, int32_t *counts,

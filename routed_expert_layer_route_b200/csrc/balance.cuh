@@ -278,7 +278,7 @@ struct RouteBackArgs {
     const int32_t *counts; // nullable [E + 1]: the losses' part is added
     const float *d_loss;   // nullable (1)
     const uint8_t *mask;   // nullable [T]
-    int T, E, k1, k2;
+    int T, E, k1, k2;      // k1 <= k2 <= E
     float c_bal, c_z;
     void *dz;              // [T x E]
     int dz_bf16;
@@ -567,7 +567,7 @@ __global__ void __launch_bounds__(kBalWarps * 32, row_ctas(N)) k_route_backward(
     const int E = a.E, Ep = (E + 3) & ~3;
     float *share = reinterpret_cast<float *>(rb_smem);  // [Ep] f_e
     float *gw = share + Ep + warp * Ep;                 // [Ep] of this warp: dL/dw, zero between rows
-    __shared__ int total;
+    __shared__ unsigned long long total;
     const float kNegInf = -__int_as_float(0x7f800000);
     for (int e = tid; e < (kBalWarps + 1) * Ep; e += kBalWarps * 32)
         share[e] = 0.0f;
@@ -578,14 +578,17 @@ __global__ void __launch_bounds__(kBalWarps * 32, row_ctas(N)) k_route_backward(
     pdl_trigger();
     float per = 0.0f;  // d_loss / N
     if (a.counts) {
-        int n = 0;
+        // 64 bits: counts summed over many batches may each come near 2^31
+        unsigned long long n = 0;
         for (int e = tid; e < E; e += kBalWarps * 32)
-            n += __ldg(&a.counts[e]);
-        n = __reduce_add_sync(0xffffffffu, n);
+            n += (unsigned)__ldg(&a.counts[e]);
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1)
+            n += __shfl_xor_sync(0xffffffffu, n, o);
         if (lane == 0)
             atomicAdd(&total, n);
         __syncthreads();
-        const float R = (float)max(total, 1);
+        const float R = total ? (float)total : 1.0f;
         for (int e = tid; e < E; e += kBalWarps * 32)
             share[e] = (float)__ldg(&a.counts[e]) / R;
         per = (a.d_loss ? __ldg(a.d_loss) : 1.0f) / (float)max(__ldg(&a.counts[E]), 1);

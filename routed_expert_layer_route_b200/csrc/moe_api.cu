@@ -2084,8 +2084,8 @@ int moe_route_backward(const float *logits, const int32_t *topk_idx, const float
         !aligned16(topk_idx) || !aligned16(dlogits) || !aligned4(d_topk_w) || !aligned4(counts) ||
         !aligned4(d_loss) || (reinterpret_cast<uintptr_t>(ws) & 255))
         return MOE_ERR_INVALID_ARG;
-    RouteBackArgs a = {logits, topk_idx, d_topk_w, counts, d_loss, token_mask, T, E, k1, k2,
-                       balance_coef, z_coef, dlogits, dz_dtype == MOE_DTYPE_BF16,
+    RouteBackArgs a = {logits, topk_idx, d_topk_w, counts, d_loss, token_mask, T, E, k1,
+                       k2 < E ? k2 : E, balance_coef, z_coef, dlogits, dz_dtype == MOE_DTYPE_BF16,
                        ws ? &static_cast<WsHeader *>(ws)->status : nullptr};
     return enqueue_route_backward(a, static_cast<cudaStream_t>(stream));
 }

@@ -266,6 +266,48 @@ def test_bad_logits_show(bad):
     assert torch.equal(dz[rows], clean[rows])
 
 
+@pytest.mark.parametrize("E", [40, 300])
+def test_all_experts_with_a_nan_at_a_given_one(E):
+    # k2 beyond E is all experts, also where the k2 set is searched for; the
+    # other rows are as without the NaN
+    z, idx, _, d_w = make(9, E, 4)
+    want, got = torch.empty(9, E, device=DEV), torch.empty(9, E, device=DEV)
+    moe.moe_route_backward(z, idx, E, d_w, want)
+    bad = z.clone()
+    bad[3, int(idx[3, 1])] = float("nan")
+    moe.moe_route_backward(bad, idx, 2 ** 31 - 1, d_w, got)
+    torch.cuda.synchronize()
+    assert torch.isnan(got[3]).any()
+    keep = [t for t in range(9) if t != 3]
+    assert torch.equal(got[keep], want[keep])
+
+
+def test_counts_of_many_batches():
+    # the counts' sum needs more than 32 bits
+    T, E, k1, k2 = 6, 16, 2, 4
+    z, idx, _, d_w = make(T, E, k1)
+    counts = torch.full((E + 1,), 2 ** 30, dtype=torch.int32, device=DEV)
+    counts[::2] = 2 ** 31 - 1
+    counts[E] = T
+    dz = torch.empty(T, E, device=DEV)
+    moe.moe_route_backward(z, idx, k2, d_w, dz, counts=counts, balance_coef=0.5, z_coef=0.01)
+    want, mag = ref.route_backward(z, idx, k2, d_w, counts, 0.5, 0.01)
+    check_dz(dz, want, mag)
+
+
+def test_a_repeated_expert_counts_each_time():
+    T, E, k1, k2 = 7, 48, 4, 8
+    z, idx, _, d_w = make(T, E, k1)
+    idx[:, 2] = idx[:, 0]
+    idx[4] = idx[4, 1]
+    counts, loss, prob, _ = balance(z, idx)
+    assert torch.equal(counts.cpu().long(), ref.balance(z, idx, None)[0].long())
+    dz = torch.empty(T, E, device=DEV)
+    moe.moe_route_backward(z, idx, k2, d_w, dz)
+    want, mag = ref.route_backward(z, idx, k2, d_w)
+    check_dz(dz, want, mag)
+
+
 def test_ids_out_of_range():
     z, idx, _, d_w = make(30, 64, 4, seed=12)
     hole = idx.clone()

@@ -3,8 +3,8 @@ gradient, and the error bounds the kernels are held to.
 
 Bounds are elementwise and count roundings: a float32 sum of K products, in
 any order and with truncating adders, is off by at most (K + 2) 2^-23 times
-the sum of the products' magnitudes; u may be carried as two bf16 parts
-(2^-16 relative); an output is rounded once (float32 2^-24, bf16 2^-8).
+the sum of the products' magnitudes; u may be carried as bf16 parts, two or
+more (2^-16 relative); an output is rounded once (float32 2^-24, bf16 2^-8).
 """
 import math
 
