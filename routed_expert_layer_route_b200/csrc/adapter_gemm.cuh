@@ -127,30 +127,113 @@ MOE_DEVINL void prefetch_tensormap(const CUtensorMap *m)
 
 MOE_DEVINL bool ag_aborted(const AGSync &sy) { return *(volatile const int *)&sy.abort != 0; }
 
-// One output alone, in float32: the row's product with W (or what y holds)
-// and its own adapter's part.
+// One output alone, in float32: its own adapter's part and the row's product
+// with W.  A NaN on the way is the output's own and stays one.
 __device__ __noinline__ float ag_one(const AdProductArgs &p, int a, int t, int o)
 {
+    const float part = a >= 0 ? ad_part(p, a, t, o) : 0.0f;
+    if (!p.w || part != part)
+        return part;
+    const uint16_t *x = p.x + (size_t)t * p.din, *w = p.w + (size_t)o * p.din;
     float v = 0.0f;
-    if (p.w) {
-        const uint16_t *x = p.x + (size_t)t * p.din, *w = p.w + (size_t)o * p.din;
-        for (int k = 0; k < p.din; k += 8) {
-            const uint4 a8 = __ldg(reinterpret_cast<const uint4 *>(x + k));
+    for (int k0 = 0; k0 < p.din && v == v; k0 += 64)
+#pragma unroll
+        for (int k = k0; k < k0 + 64; k += 8) {
+            const uint4 a8 = ad_chunk(x, k, p.din, true), w8 = ad_chunk(w, k, p.din, true);
             const float xv[8] = {bf16lo(a8.x), bf16hi(a8.x), bf16lo(a8.y), bf16hi(a8.y),
                                  bf16lo(a8.z), bf16hi(a8.z), bf16lo(a8.w), bf16hi(a8.w)};
-            v = dot8_bf16(__ldg(reinterpret_cast<const uint4 *>(w + k)), xv, v);
+            v = dot8_bf16(w8, xv, v);
         }
-    }
-    return a >= 0 ? v + ad_part(p, a, t, o) : v;
+    return v + part;
 }
 
-// The NaNs among a row's 32 outputs from o on once more.
-__device__ __noinline__ void ag_again(const AdProductArgs &p, float *v, int t, int o)
+// A warp: the NaNs among 32 outputs from o on (v) of rows t0 + lane once more,
+// each lane its own adapter's part of its row, the product with W of all rows
+// by matrix instructions (fragments straight from memory).  A broken adapter
+// makes every tile take this that it has a row in: 8192 rows of 4096 to 4096,
+// one of 16 adapters all inf, rows interleaved: 12.7 ms (214 output by output).
+__device__ __noinline__ void ag_again(const AdProductArgs &p, float *v, int t0, int o)
 {
-    const int a = adapter_of(p.adapter, t, p.n, nullptr);
-    for (int j = 0; j < 32 && o + j < p.dout; ++j)
-        if (v[j] != v[j])
-            v[j] = ag_one(p, a, t, o + j);
+    const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3, t = t0 + lane;
+    const int a = t < p.T ? adapter_of(p.adapter, t, p.n, nullptr) : -1;
+    uint32_t left = 0;  // the outputs whose product is missing
+    for (int j = 0; j < 32; ++j)
+        if (t < p.T && o + j < p.dout && v[j] != v[j])
+            left |= 1u << j;
+    const int rp = ad_rp(p.r);
+    const uint16_t *u = p.parts + (size_t)(a >= 0 ? t : 0) * kAdParts * rp;
+#pragma unroll 1
+    for (int j = 0; j < 32; j += 8) {  // eight outputs at a time
+        if (!(left >> j & 0xffu))
+            continue;
+        float part[8] = {};
+        const uint16_t *b = p.b + (size_t)(a >= 0 ? a : 0) * p.r * p.dout + o + j;
+        for (int e = 0; e < (a >= 0 ? p.r : 0); ++e) {
+            float x = bf16_to_f32(__ldcg(&u[e]));
+#pragma unroll
+            for (int i = 1; i < kAdParts; ++i)
+                x += bf16_to_f32(__ldcg(&u[i * rp + e]));
+            const uint4 w = __ldg(reinterpret_cast<const uint4 *>(b + (size_t)e * p.dout));
+            const float wv[8] = {bf16lo(w.x), bf16hi(w.x), bf16lo(w.y), bf16hi(w.y),
+                                 bf16lo(w.z), bf16hi(w.z), bf16lo(w.w), bf16hi(w.w)};
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                part[k] = fmaf(x, wv[k], part[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (left >> (j + k) & 1u) {
+                v[j + k] = part[k];
+                if (part[k] != part[k])  // its own: it stays one
+                    left &= ~(1u << (j + k));
+            }
+    }
+    if (!p.w || !__any_sync(0xffffffffu, left != 0))
+        return;
+#pragma unroll 1
+    for (int m = 0; m < 2; ++m) {  // rows t0 + 16 m + 0 .. 15
+        const int ta = t0 + 16 * m + g, tb = ta + 8;
+        float sum[4][4] = {};
+        bool some = true;
+#pragma unroll 1
+        for (int c0 = 0; c0 < p.din && some; c0 += 8 * kAdChunk) {
+            float acc[4][4] = {};
+#pragma unroll 1
+            for (int c = c0; c < min(p.din, c0 + 8 * kAdChunk); c += kAdChunk) {
+                const int k = c + 8 * q;
+                const uint4 xa = ad_chunk(p.x + (size_t)ta * p.din, k, p.din, ta < p.T);
+                const uint4 xb = ad_chunk(p.x + (size_t)tb * p.din, k, p.din, tb < p.T);
+                uint4 w[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    w[i] = ad_chunk(p.w + (size_t)(o + 8 * i + g) * p.din, k, p.din,
+                                    o + 8 * i + g < p.dout);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    mma_bf16(acc[i], xa.x, xb.x, xa.y, xb.y, w[i].x, w[i].y);
+                    mma_bf16(acc[i], xa.z, xb.z, xa.w, xb.w, w[i].z, w[i].w);
+                }
+            }
+            some = false;  // rows of NaN alone end here
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    sum[i][h] += acc[i][h];
+                    some |= sum[i][h] == sum[i][h];
+                }
+            some = __any_sync(0xffffffffu, some);
+        }
+        // from the fragments to a row a lane
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+            const int from = (lane & 7) * 4 + (j & 7) / 2;
+            const float lo = __shfl_sync(0xffffffffu, sum[j >> 3][j & 1], from);
+            const float hi = __shfl_sync(0xffffffffu, sum[j >> 3][2 + (j & 1)], from);
+            if ((left >> j & 1u) && lane >> 4 == m)
+                v[j] += lane & 8 ? hi : lo;
+        }
+    }
 }
 
 MOE_DEVINL uint32_t ag_word(uint32_t w) { return w; }
@@ -600,15 +683,23 @@ __global__ void __launch_bounds__(kAGThreads, 1)
 #pragma unroll
                 for (int j = 0; j < 32; ++j)
                     bad |= v[j] != v[j];
-                if (bad && t < p.T) {
-                    float w[32];
+                if (__any_sync(0xffffffffu, bad && t < p.T)) {
+                    // (through memory: nothing of the rare call costs the others registers)
+                    constexpr int kSum = BN == 128 ? 32 : 0;
+                    float w[32 + kSum];
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
+                    for (int j = 0; j < 32; ++j) {
                         w[j] = v[j];
-                    ag_again(p, w, t, o);
+                        if (BN == 128)
+                            w[kSum + j] = sum[1][j];
+                    }
+                    ag_again(p, w, t - lane, o);
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
+                    for (int j = 0; j < 32; ++j) {
                         v[j] = w[j];
+                        if (BN == 128)
+                            sum[1][j] = w[kSum + j];
+                    }
                 }
                 if (p.bias) {
 #pragma unroll

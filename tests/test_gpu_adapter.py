@@ -158,6 +158,29 @@ def test_bad_numbers_stay_in_their_rows(T, dout):
     assert torch.isnan(da[3, 2]).all() and torch.isfinite(da[3, 3:]).all() and torch.isnan(db[2, 0]).all() and torch.isfinite(db[2, 1:]).all()
 
 
+@pytest.mark.parametrize("T,din,dout", [(600, 1000, 520), (3000, 264, 2056), (70, 2056, 136)], ids=str)
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("base", [True, False], ids=["product", "beside"])
+def test_a_broken_adapter_in_every_tile(T, din, dout, dtype, base):
+    # the rows of the others, whose products with it are 0 x inf, keep their values
+    c = ref.Case(T, din, dout, 20, 3, seed=5)
+    c.adapter = (torch.arange(T, device=DEV) % 4).int()
+    c.adapter[c.adapter == 3] = ref.EMPTY
+    product = None if base else torch.randn(T, dout, device=DEV).to(dtype)
+    want, e, _, _ = ref.linear(c.x, c.w if base else None, c.bias if base else None, c.adapter, c.a,
+                               c.b, c.scale, product=product)
+    c.b[1, 7] = float("inf")
+    c.b[1, 8] = float("-inf")
+    c.x[5::60] = float("nan")
+    y, _, ws = run_linear(c, dtype, bias=base, product=product)
+    row = torch.arange(T, device=DEV)
+    broken, own = row % 4 == 1, row % 60 == 5
+    assert not torch.isfinite(y[broken]).any()
+    fine = ~broken & ~own
+    ref.check(y[fine], want[fine], e[fine])
+    assert moe.moe_read_device_status(ws) == 0
+
+
 @pytest.mark.parametrize("T", [1, 20, 70, 400])
 def test_ids_out_of_range_count_as_none(T):
     c = ref.Case(T, 128, 64, 8, 3, seed=5)
