@@ -15,8 +15,8 @@
 //
 // Zeros do not silence a NaN or inf: 0 x inf is NaN, so a broken adapter
 // would reach the other rows of its tile.  Every such product is a NaN, so
-// the epilogue computes an output that came out NaN once more, alone, from
-// its own row and adapter.
+// the epilogue computes an output that came out NaN once more, from its own
+// row and adapter alone.
 //
 // Where the tiles leave more than half of the pairs idle (few rows, or few
 // outputs as a router has), K is split over several pairs, which leave their
@@ -39,7 +39,8 @@
 // blocks of a row block side by side in time.  Roles of a CTA's 448 threads:
 //   warps 0-3, 6-9  epilogue (two warps a quarter of the tensor-memory lanes)
 //   warp 4          TMA producer of X and W
-//   warp 5          tensor memory; in CTA 0 one thread issues the MMAs
+//   warp 5          tensor memory; one thread issues the MMAs (CTA 0) or says
+//                   that U's copies have landed (CTA 1)
 //   warps 10-13     the U operand, the list of a tile's adapters, TMA of B
 // X and W need nothing of the inner kernel and are loaded while it runs (it
 // lets this kernel start after its own wait); the U warps and the epilogue
@@ -47,11 +48,15 @@
 //
 // Bound by the matrix instructions for large tiles: 8192 rows, 4096 to 4096,
 // bf16: 187 us of the call's 226 in here, 1.47 PFLOP/s.  A K block of a tile
-// takes 0.36 to 0.38 us, a unit of adapters about 0.7 once the buffers that
+// takes 0.36 to 0.38 us, a unit of adapters about 0.5 once the buffers that
 // were ready are used up (one way from "empty" to the products and back),
 // which is what many adapters in a tile cost: the same rows with every row
-// another request's take 386 us.  Small calls are bound by the chain of
-// launches, set-up and waits, 10 to 11 us for 100 rows.
+// another request's take 340 us.  U goes to its buffers by asynchronous copies
+// that the MMA thread (in the other CTA a thread that passes it on) waits for
+// and fences: with loads to registers, stores and a fence in the U threads,
+// which waits for their next loads, a unit took 0.7 us and these rows 360.
+// Small calls are bound by the chain of launches, set-up and waits: 15 us for
+// 100 rows, 2048 to 2048.
 #pragma once
 #include "adapter.cuh"
 #include "gemm_pair.cuh"
@@ -79,7 +84,8 @@ struct AGShape {
 struct AGSync {
     uint64_t full[6];             // CTA 0: both CTAs' tiles of stage s landed
     uint64_t empty[6];            // each CTA: the MMAs reading stage s finished
-    uint64_t ufull[kAGUBufs];     // CTA 0: both CTAs' U warps have written
+    uint64_t ucopy[kAGUBufs];     // each CTA: its U warps' copies have landed
+    uint64_t ufull[kAGUBufs];     // CTA 0: the other CTA's too
     uint64_t bfull[kAGBBufs];     // CTA 0: both CTAs' copies of B landed
     uint64_t uempty[kAGUBufs];    // each CTA: the MMAs reading the buffer finished
     uint64_t acc_full[2];         // each CTA: accumulator set b is complete
@@ -118,6 +124,14 @@ MOE_DEVINL void tma_load_3d_pair(void *dst, const CUtensorMap *map, int x, int y
         " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_addr(dst)),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_caddr), "r"(x), "r"(y), "r"(z)
         : "memory");
+}
+
+// Arrive on `bar` (one of its counted arrivals) when this thread's copies so
+// far have landed.
+MOE_DEVINL void cp_async_arrive(uint64_t *bar)
+{
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar))
+                 : "memory");
 }
 
 MOE_DEVINL void prefetch_tensormap(const CUtensorMap *m)
@@ -313,7 +327,8 @@ __global__ void __launch_bounds__(kAGThreads, 1)
             mbar_init(&sy.empty[s], 1);
         }
         for (int b = 0; b < kAGUBufs; ++b) {
-            mbar_init(&sy.ufull[b], 8);  // four U warps of each CTA
+            mbar_init(&sy.ucopy[b], 128 + 1);  // the U threads' copies, u_what
+            mbar_init(&sy.ufull[b], 1);
             mbar_init(&sy.uempty[b], 1);
         }
         for (int b = 0; b < kAGBBufs; ++b)
@@ -411,10 +426,13 @@ __global__ void __launch_bounds__(kAGThreads, 1)
                     bool more = it % splits == 0 && sg == nseg - 1;
                     auto unit = [&]() {
                         const int b = ub % kAGUBufs;
-                        if (!mbar_wait_cluster(&sy.ufull[b], (ub / kAGUBufs) & 1, status)) {
+                        const uint32_t ph = (ub / kAGUBufs) & 1;
+                        if (!mbar_wait(&sy.ucopy[b], ph, status) ||
+                            !mbar_wait_cluster(&sy.ufull[b], ph, status)) {
                             sy.abort = 1;
                             return;
                         }
+                        fence_proxy_async_smem();  // the copies, for the MMAs
                         tc_fence_after();
                         const int what = *(volatile int *)&sy.u_what[b];
                         const uint32_t st = smem_addr(ubuf + (size_t)b * kAGTileA);
@@ -465,6 +483,23 @@ __global__ void __launch_bounds__(kAGThreads, 1)
             }
             umma_commit_pair_both(&sy.drained);
             mbar_wait(&sy.drained, 0, status);
+        } else if (lane == 0) {
+            // CTA 1: tells CTA 0 of the units of U that have landed here
+            uint32_t ub = 0;
+            for (int it = pair; it < items && !ag_aborted(sy); it += pairs) {
+                bool more = it % splits == 0;
+                while (more) {
+                    const int b = ub % kAGUBufs;
+                    if (!mbar_wait(&sy.ucopy[b], (ub / kAGUBufs) & 1, status)) {
+                        sy.abort = 1;
+                        break;
+                    }
+                    fence_proxy_async_smem();
+                    more = !(*(volatile int *)&sy.u_what[b] & 2);
+                    mbar_arrive_cluster(cluster_addr(&sy.ufull[b], 0));
+                    ++ub;
+                }
+            }
         }
     } else if (warp >= kAGWarpU) {
         // ------------------------------------------------------------ U and B
@@ -516,13 +551,6 @@ __global__ void __launch_bounds__(kAGThreads, 1)
             const int units = sy.count * nch;
             const int o0 = i % ncol * BN + (int)rank * (BN / 2);
             const uint16_t *urow = p.parts + (size_t)(a >= 0 ? t : 0) * kAdParts * rp;
-            // this row's next two units of u, loaded before their turn comes
-            uint4 own[2][2 * kAdParts] = {};
-            auto load_own = [&](uint4(&to)[2 * kAdParts], int j) {
-#pragma unroll
-                for (int c = 0; c < 2 * kAdParts; ++c)
-                    to[c] = __ldcg(reinterpret_cast<const uint4 *>(urow + c / 2 * rp + j) + c % 2);
-            };
             // B of unit u (one thread).  Its buffer was unit u - kAGBBufs's, whose
             // MMAs are complete once U's buffer of unit u - kAGBBufs + kAGUBufs
             // has come back empty, so a unit's copy starts kAGUBufs units ahead
@@ -550,11 +578,6 @@ __global__ void __launch_bounds__(kAGThreads, 1)
                 pdl_trigger();
                 waited = true;
             }
-            if (a >= 0) {
-                load_own(own[0], 0);
-                if (rp > 16)
-                    load_own(own[1], 16);
-            }
             int u0 = 0, li = 0, j = 0;  // the unit: its adapter in the list, its first rank
             do {
                 const int b = ub % kAGUBufs;
@@ -562,31 +585,23 @@ __global__ void __launch_bounds__(kAGThreads, 1)
                 // one lane waits for its warp
                 int ok = 1;
                 if (lane == 0)
-                    ok = mbar_wait_cluster(&sy.uempty[b], ((ub / kAGUBufs) & 1) ^ 1, status);
+                    ok = mbar_wait(&sy.uempty[b], ((ub / kAGUBufs) & 1) ^ 1, status);
                 if (!__shfl_sync(0xffffffffu, ok, 0)) {
                     sy.abort = 1;
                     break;
                 }
-                uint8_t *st = ubuf + (size_t)b * kAGTileA;
-                if (ut == 0 && lead)
-                    sy.u_what[b] = (e >= 0 ? 1 : 0) | (u0 + 1 >= units ? 2 : 0);
+                const uint32_t st = smem_addr(ubuf + (size_t)b * kAGTileA) + ut * 128;
+                const bool own = a >= 0 && a == e;
 #pragma unroll
                 for (int c = 0; c < 2 * kAdParts; ++c)
-                    *reinterpret_cast<uint4 *>(st + ut * 128 + ((c ^ (ut & 7)) << 4)) =
-                        a >= 0 && a == e ? own[0][c] : make_uint4(0u, 0u, 0u, 0u);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive_cluster(cluster_addr(&sy.ufull[b], 0));
+                    cp_async16(st + ((c ^ (ut & 7)) << 4), urow + c / 2 * rp + j + c % 2 * 8, own);
+                cp_async_arrive(&sy.ucopy[b]);
+                if (ut == 0) {
+                    sy.u_what[b] = (e >= 0 ? 1 : 0) | (u0 + 1 >= units ? 2 : 0);
+                    mbar_arrive(&sy.ucopy[b]);
+                }
                 if (ut == 0 && u0 + kAGUBufs < units)
                     load_b();
-                if (a >= 0 && a == e) {
-#pragma unroll
-                    for (int c = 0; c < 2 * kAdParts; ++c)
-                        own[0][c] = own[1][c];
-                    if (j + 32 < rp)  // after the fence, which waits for loads
-                        load_own(own[1], j + 32);
-                }
                 j += 16;
                 if (j >= rp) {
                     j = 0;
@@ -599,6 +614,8 @@ __global__ void __launch_bounds__(kAGThreads, 1)
             if (ag_aborted(sy))
                 break;
         }
+        cp_async_commit();
+        cp_async_wait<0>();
     } else {
         // ------------------------------------------------------------ epilogue
         const int lq = warp & 3, eh = warp >= 6;

@@ -55,14 +55,6 @@ constexpr int kAOThreads = (kAOWarps + 1) * 32;
 constexpr int kAOBlock = kAORows * 128;      // 64 values of every row
 constexpr int kAOStage = (kAdParts + kAOCols / 64) * kAOBlock;
 
-// Arrive on `bar` (one of its counted arrivals) when this thread's copies so
-// far have landed.
-MOE_DEVINL void cp_async_arrive(uint64_t *bar)
-{
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar))
-                 : "memory");
-}
-
 constexpr int kAOHalfPitch = kAOCols + 4;  // floats of a lower-half row on its way to the upper
 
 struct AOSync {
