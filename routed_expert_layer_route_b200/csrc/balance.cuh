@@ -19,7 +19,7 @@
 // Both kernels give a token one warp and hold its E logits in registers, so
 // each logit is read once; sums over a token are warp reductions in float32.
 // T = 65536, E = 512: k_balance 28 us, 4.9 TB/s, bound by the read (76% of the
-// copy bandwidth); k_route_backward with both parts, k1 = 5, k2 = 20, 87 us,
+// copy bandwidth); k_route_backward with both parts, k1 = 5, k2 = 20, 85 us,
 // bound by its instructions (about 950 a row, 400 of them on the half-rate
 // comparison and logic pipe; reading and writing alone would take 32 us).
 // Small calls take 4 to 5 us, a launch and one pass of dependent loads.
@@ -271,6 +271,10 @@ __global__ void __launch_bounds__(kBalWarps * 32, row_ctas(N)) k_balance(Balance
 inline size_t balance_smem_bytes(int E) { return sizeof(float) * kBalWarps * E + sizeof(int) * (E + 1); }
 
 // ---------------------------------------------------------------------------
+constexpr int kRouteWarps = 8;
+// as row_ctas; four CTAs spill a little and still win (65536 rows of 512: 85 us, 87 with three)
+constexpr int route_ctas(int N) { return N <= 16 ? 4 : 2; }
+
 struct RouteBackArgs {
     const float *logits;   // [T x E]
     const int32_t *idx;    // [T x k1]
@@ -560,7 +564,7 @@ __device__ __noinline__ void route_row_general(const RouteBackArgs &a, int t, in
 }
 
 template <int VEC, int N>
-__global__ void __launch_bounds__(kBalWarps * 32, row_ctas(N)) k_route_backward(RouteBackArgs a)
+__global__ void __launch_bounds__(kRouteWarps * 32, route_ctas(N)) k_route_backward(RouteBackArgs a)
 {
     extern __shared__ __align__(16) uint8_t rb_smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -569,7 +573,7 @@ __global__ void __launch_bounds__(kBalWarps * 32, row_ctas(N)) k_route_backward(
     float *gw = share + Ep + warp * Ep;                 // [Ep] of this warp: dL/dw, zero between rows
     __shared__ unsigned long long total;
     const float kNegInf = -__int_as_float(0x7f800000);
-    for (int e = tid; e < (kBalWarps + 1) * Ep; e += kBalWarps * 32)
+    for (int e = tid; e < (kRouteWarps + 1) * Ep; e += kRouteWarps * 32)
         share[e] = 0.0f;
     if (tid == 0)
         total = 0;
@@ -580,7 +584,7 @@ __global__ void __launch_bounds__(kBalWarps * 32, row_ctas(N)) k_route_backward(
     if (a.counts) {
         // 64 bits: counts summed over many batches may each come near 2^31
         unsigned long long n = 0;
-        for (int e = tid; e < E; e += kBalWarps * 32)
+        for (int e = tid; e < E; e += kRouteWarps * 32)
             n += (unsigned)__ldg(&a.counts[e]);
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1)
@@ -589,14 +593,14 @@ __global__ void __launch_bounds__(kBalWarps * 32, row_ctas(N)) k_route_backward(
             atomicAdd(&total, n);
         __syncthreads();
         const float R = total ? (float)total : 1.0f;
-        for (int e = tid; e < E; e += kBalWarps * 32)
+        for (int e = tid; e < E; e += kRouteWarps * 32)
             share[e] = (float)__ldg(&a.counts[e]) / R;
         per = (a.d_loss ? __ldg(a.d_loss) : 1.0f) / (float)max(__ldg(&a.counts[E]), 1);
         __syncthreads();
     }
     const float cb = a.c_bal * (float)E;
 
-    for (int t = blockIdx.x * kBalWarps + warp; t < a.T; t += gridDim.x * kBalWarps) {
+    for (int t = blockIdx.x * kRouteWarps + warp; t < a.T; t += gridDim.x * kRouteWarps) {
         float v[N];  // the logits, then the gradient
         float m = kNegInf;
         bool live = !a.mask || a.mask[t];
@@ -713,7 +717,7 @@ __global__ void __launch_bounds__(kBalWarps * 32, row_ctas(N)) k_route_backward(
 
 inline size_t route_backward_smem_bytes(int E)
 {
-    return sizeof(float) * (kBalWarps + 1) * ((E + 3) & ~3);
+    return sizeof(float) * (kRouteWarps + 1) * ((E + 3) & ~3);
 }
 
 }  // namespace moe

@@ -2000,9 +2000,9 @@ static int bal_check(int T, int E, int k1)
         CALL(1, 32);                          \
     } while (0)
 
-static int row_grid(int T, int N)
+static int row_grid(int T, int warps, int ctas)
 {
-    const int g = (T + kBalWarps - 1) / kBalWarps, most = 148 * row_ctas(N);
+    const int g = (T + warps - 1) / warps, most = 148 * ctas;
     return g < most ? g : most;
 }
 
@@ -2010,8 +2010,8 @@ static int enqueue_balance(const BalanceArgs &a, cudaStream_t s)
 {
     const int E = a.E;
 #define MOE_BAL(VEC, N)                                                                        \
-    return launch(k_balance<VEC, N>, dim3(row_grid(a.T, N)), dim3(kBalWarps * 32),                \
-                  balance_smem_bytes(E), s, kPdl, a)
+    return launch(k_balance<VEC, N>, dim3(row_grid(a.T, kBalWarps, row_ctas(N))),               \
+                  dim3(kBalWarps * 32), balance_smem_bytes(E), s, kPdl, a)
     MOE_ROW_VARIANTS(MOE_BAL);
 #undef MOE_BAL
 }
@@ -2020,8 +2020,8 @@ static int enqueue_route_backward(const RouteBackArgs &a, cudaStream_t s)
 {
     const int E = a.E;
 #define MOE_RB(VEC, N)                                                                         \
-    return launch(k_route_backward<VEC, N>, dim3(row_grid(a.T, N)), dim3(kBalWarps * 32),         \
-                  route_backward_smem_bytes(E), s, kPdl, a)
+    return launch(k_route_backward<VEC, N>, dim3(row_grid(a.T, kRouteWarps, route_ctas(N))),     \
+                  dim3(kRouteWarps * 32), route_backward_smem_bytes(E), s, kPdl, a)
     MOE_ROW_VARIANTS(MOE_RB);
 #undef MOE_RB
 }
