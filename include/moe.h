@@ -47,8 +47,10 @@
  *    status word; read it with moe_read_device_status.
  *  - Workspace: `ws` is caller-owned device memory of at least
  *    moe_workspace_size(...) bytes, 256-byte aligned, initialised once with
- *    moe_workspace_init before its first use.  Calls leave it initialised.
- *    Calls that share one workspace must be ordered on one stream.
+ *    moe_workspace_init before its first use.  Calls leave it initialised:
+ *    one workspace serves calls of every kind and size that it has the bytes
+ *    for, in any order.  Calls that share one workspace must be ordered on
+ *    one stream.
  */
 #ifndef MOE_H
 #define MOE_H

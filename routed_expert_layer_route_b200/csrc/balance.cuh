@@ -95,6 +95,7 @@ struct BalanceArgs {
     int32_t *counts;            // out [E + 1]
     float *loss;                // out [3]
     float *prob;                // nullable out [E]
+    // WsKept's
     unsigned long long *p_acc;  // [E] zero between calls
     int *n_acc;                 // [E + 1] zero between calls
     unsigned *arrive;           // zero between calls

@@ -51,6 +51,22 @@ struct WsHeader {
 static_assert(sizeof(WsHeader) == 12288, "header is 12 KiB");
 static_assert(offsetof(WsHeader, xcnt) == 4096, "spread counters on whole lines");
 
+// Behind the header: what calls need zero when they start and leave zero for
+// the next.  It lies at one place in every workspace, whatever the shapes, and
+// no call has scratch there (scratch begins at kWsScratch), so that one
+// workspace serves calls of all kinds and sizes in any order.
+constexpr int kMtMaxT = 8;      // most tokens of the decode kernels
+constexpr int kMaxHidden = 8192;
+constexpr int kBalMaxGrid = 148 * 4;  // CTAs of the balance loss
+struct WsKept {
+    float decode_acc[kMtMaxT * kMaxHidden];  // the decode kernels' sums [8 x d]
+    unsigned long long bal_p[kMaxExperts];   // the balance loss's probabilities,
+    int bal_n[kMaxExperts + 1];              //   counts
+    unsigned bal_arrive;                     //   and arrivals
+    double bal_z[kBalMaxGrid];               //   (written before it is read: not kept)
+};
+constexpr size_t kWsScratch = (sizeof(WsHeader) + sizeof(WsKept) + 255) / 256 * 256;
+
 // Bounded waits give up after this many nanoseconds (globaltimer) and record
 // MOE_ERR_TIMEOUT; no correct launch comes anywhere near it.  The limit is a
 // device variable (2 s) that a test hook may shorten.

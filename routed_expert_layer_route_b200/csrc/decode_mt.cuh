@@ -45,7 +45,6 @@
 
 namespace moe {
 
-constexpr int kMtMaxT = 8;        // tokens per call
 constexpr int kMtMaxSlots = 64;   // T * k1
 constexpr int kMtMaxRowVec = 2;   // 16-byte row vectors per lane (d <= 5632)
 constexpr int kMtMaxCh = 8;       // channels per stage

@@ -27,9 +27,9 @@
 namespace moe {
 
 // ------------------------------------------------------------------ limits
-constexpr int kMaxE = 1024;
+constexpr int kMaxE = kMaxExperts;
 constexpr int kMaxK1 = 32;
-constexpr int kMinD = 64, kMaxD = 8192;
+constexpr int kMinD = 64, kMaxD = kMaxHidden;
 constexpr int kMinI = 16, kMaxI = 8192;
 constexpr int kMaxT = 1 << 20;
 
@@ -37,7 +37,7 @@ static inline size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
 
 struct WsLayout {
     size_t logits, idx, w, offsets, sorted_slot, slot_pos, uniq_count, uniq_list, h, out, y_acc,
-        hist, ctk, dyacc, total;
+        hist, ctk, total;
 };
 
 static inline int perm_chunks(int T) { return (T + kPermTok - 1) / kPermTok; }
@@ -45,11 +45,8 @@ static inline int perm_chunks(int T) { return (T + kPermTok - 1) / kPermTok; }
 static WsLayout ws_layout(int T, int d, int E, int I, int k1)
 {
     WsLayout L;
-    size_t o = sizeof(WsHeader);
+    size_t o = kWsScratch;
     const size_t n = (size_t)T * k1;
-    // the decode kernels' accumulator (kMtMaxT tokens, kept zero between
-    // calls), first after the header: the same place for every T
-    L.dyacc = o;       o = align256(o + sizeof(float) * (size_t)kMtMaxT * d);
     L.logits = o;      o = align256(o + sizeof(float) * (size_t)T * E);
     L.idx = o;         o = align256(o + sizeof(int32_t) * n);
     L.w = o;           o = align256(o + sizeof(float) * n);
@@ -72,6 +69,8 @@ static inline P *at(void *ws, size_t off)
 {
     return reinterpret_cast<P *>(reinterpret_cast<char *>(ws) + off);
 }
+
+static inline WsKept *ws_kept(void *ws) { return at<WsKept>(ws, sizeof(WsHeader)); }
 
 static inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
@@ -316,7 +315,7 @@ static int enqueue_decode(const void *x, const void *wr, const float *bias, floa
     a.slot_pos = at<int32_t>(ws, L.slot_pos);
     a.uniq_count = at<int32_t>(ws, L.uniq_count);
     a.uniq_list = at<int32_t>(ws, L.uniq_list);
-    a.yacc = at<float>(ws, L.dyacc);
+    a.yacc = ws_kept(ws)->decode_acc;
     a.y = y;
     a.y_dtype = y_dtype;
     a.vk = vk;
@@ -365,7 +364,7 @@ static int enqueue_decode_mt(const void *x, const void *wr, const float *bias, f
     a.idx_copy = idx_copy;
     a.w_copy = w_copy;
     a.count = count;
-    a.yacc = at<float>(ws, L.dyacc);
+    a.yacc = ws_kept(ws)->decode_acc;
     a.y = y;
     a.y_dtype = y_dtype;
     a.T = T;
@@ -668,7 +667,7 @@ static int route_impl(const void *x_bf16, const void *w_router_bf16, const float
         if (!logits) {
             if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255))
                 return MOE_ERR_INVALID_ARG;
-            const size_t need = sizeof(WsHeader) + align256(sizeof(float) * (size_t)T * E);
+            const size_t need = kWsScratch + align256(sizeof(float) * (size_t)T * E);
             if (ws_bytes < need)
                 return MOE_ERR_WORKSPACE_TOO_SMALL;
         }
@@ -683,7 +682,7 @@ static int route_impl(const void *x_bf16, const void *w_router_bf16, const float
         return rc;
     const float *z = logits;
     if (x_bf16) {
-        float *zbuf = logits ? logits : at<float>(ws, sizeof(WsHeader));
+        float *zbuf = logits ? logits : at<float>(ws, kWsScratch);
         if ((rc = enqueue_logits(x_bf16, w_router_bf16, bias, zbuf, nullptr, T, d, E, s)) != MOE_OK)
             return rc;
         z = zbuf;
@@ -761,11 +760,10 @@ int moe_permute(const int32_t *topk_idx, int T, int k1, int E, int32_t *expert_o
         return rc;
     PermOut po = {expert_offsets, sorted_slot, slot_pos, nullptr, nullptr};
     int *status = ws ? &static_cast<WsHeader *>(ws)->status : nullptr;
-    // many slots and room for the chunk counts after the header: chunked kernels
+    // many slots and room for the chunk counts: chunked kernels
     const size_t hist_bytes = sizeof(int) * (size_t)perm_chunks(T) * E;
-    if ((long)T * k1 > 4096 && ws && ws_bytes >= sizeof(WsHeader) + hist_bytes)
-        return enqueue_perm_parallel(topk_idx, T, k1, E, at<int>(ws, sizeof(WsHeader)), po, status,
-                                     s);
+    if ((long)T * k1 > 4096 && ws && ws_bytes >= kWsScratch + hist_bytes)
+        return enqueue_perm_parallel(topk_idx, T, k1, E, at<int>(ws, kWsScratch), po, status, s);
     return launch(k_permute, dim3(1), dim3(1024), permute_smem_bytes(E, T), s, true, topk_idx, T,
                   k1, E, po, status);
 }
@@ -1263,7 +1261,7 @@ int moe_test_expert_stream(const void *x_bf16, const void *w_gate_bf16, const vo
         a.slot_pos = at<int32_t>(ws, L.slot_pos);
         a.uniq_count = at<int32_t>(ws, L.uniq_count);
         a.uniq_list = at<int32_t>(ws, L.uniq_list);
-            a.yacc = at<float>(ws, L.dyacc);
+            a.yacc = ws_kept(ws)->decode_acc;
         a.y = y;
         a.y_dtype = y_dtype;
         a.hdr = static_cast<WsHeader *>(ws);
@@ -1562,7 +1560,7 @@ static int ad_piece_rows(int T, int blocks)
 static AdLayout ad_layout(int T, int din, int dout, int r, int n)
 {
     AdLayout L;
-    size_t o = sizeof(WsHeader);
+    size_t o = kWsScratch;
     const size_t rows = (size_t)T;
     const size_t rp = (size_t)((r + 15) & ~15), both = (size_t)r * (din + dout);
     L.parts = o;    o = align256(o + sizeof(uint16_t) * kAdParts * rows * rp);
@@ -1955,24 +1953,6 @@ int moe_adapter_backward(const void *dy_bf16, const void *x_bf16, const void *w_
 // ========================================================================== router training
 namespace moe {
 
-struct BalLayout {
-    size_t p_acc, n_acc, arrive, z_part, total;
-};
-
-constexpr int kBalMaxGrid = 148 * 4;  // row_ctas at most on every SM
-
-static BalLayout bal_layout(int E)
-{
-    BalLayout L;
-    size_t o = sizeof(WsHeader);
-    L.p_acc = o;   o = align256(o + sizeof(unsigned long long) * (size_t)E);
-    L.n_acc = o;   o = align256(o + sizeof(int32_t) * (size_t)(E + 1));
-    L.arrive = o;  o = align256(o + sizeof(unsigned));
-    L.z_part = o;  o = align256(o + sizeof(double) * kBalMaxGrid);
-    L.total = o;
-    return L;
-}
-
 static int bal_check(int T, int E, int k1)
 {
     if (T < 0 || T > kMaxT || E < 1 || E > kMaxE)
@@ -2032,7 +2012,7 @@ extern "C" {
 
 size_t moe_balance_workspace_size(int T, int E)
 {
-    return bal_check(T, E, 1) == MOE_OK ? bal_layout(E).total : 0;
+    return bal_check(T, E, 1) == MOE_OK ? kWsScratch : 0;
 }
 
 int moe_balance_loss(const float *logits, const int32_t *topk_idx, const unsigned char *token_mask,
@@ -2055,12 +2035,11 @@ int moe_balance_loss(const float *logits, const int32_t *topk_idx, const unsigne
     }
     if (!logits || !topk_idx || !aligned16(logits) || !aligned16(topk_idx))
         return MOE_ERR_INVALID_ARG;
-    const BalLayout L = bal_layout(E);
-    if ((rc = ad_check_ws(ws, ws_bytes, L.total)) != MOE_OK)
+    if ((rc = ad_check_ws(ws, ws_bytes, kWsScratch)) != MOE_OK)
         return rc;
+    WsKept *kept = ws_kept(ws);
     BalanceArgs a = {logits, topk_idx, token_mask, T, E, k1, balance_coef, z_coef, counts, loss,
-                     prob_mean, at<unsigned long long>(ws, L.p_acc), at<int>(ws, L.n_acc),
-                     at<unsigned>(ws, L.arrive), at<double>(ws, L.z_part),
+                     prob_mean, kept->bal_p, kept->bal_n, &kept->bal_arrive, kept->bal_z,
                      &static_cast<WsHeader *>(ws)->status};
     return enqueue_balance(a, s);
 }
