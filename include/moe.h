@@ -365,7 +365,10 @@ int moe_noalloc_read_status(int *status_out, void *stream);
  *   transposed weights (laid out once, they are frozen), needed with dx.
  *   dx NULL: not computed.  w_t_bf16 NULL with dx: dx is read and A_a^T v[t]
  *   added to it.  d_lora_a and d_lora_b are each nullable and are
- *   overwritten; adapters without rows get zeros (T = 0: all of them). */
+ *   overwritten; adapters without rows get zeros (T = 0: all of them).
+ * A NaN or inf in a row (of x, dy or u) or in an adapter's matrices shows
+ *   where the formulas put it -- in its own row's y, u and dx and in its own
+ *   adapter's gradients -- and nowhere else; such calls take longer. */
 size_t moe_adapter_workspace_size(int T, int din, int dout, int r, int n);
 int moe_adapter_linear(const void *x_bf16, const void *w_bf16, const float *bias,
                        const int32_t *adapter, const void *lora_a_bf16, const void *lora_b_bf16,

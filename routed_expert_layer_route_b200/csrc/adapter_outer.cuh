@@ -16,6 +16,11 @@
 // (relative error at 8192 rows 8.6e-7 where that gave 1.3e-6; a float32
 // product 7.9e-7); the epilogue adds the halves.
 //
+// An infinity in z meets the zeros and, where u has fewer bits, parts of 0:
+// the sums of its column come out NaN.  What came out NaN is computed once more
+// from u itself (ao_again), so an infinity gives what the formula says and a NaN
+// stays one.
+//
 // A CTA sums one piece (up to `rows` rows of one adapter) for 256 columns and
 // 64 ranks (blockIdx.z).  Adapters of one piece are stored at once; the pieces
 // of larger ones go to scratch, where k_ad_outer_join adds them in order, so
@@ -68,6 +73,62 @@ struct AOSync {
 // the zeros, the stages (afterwards the lower half's sums), the barriers
 inline size_t ao_smem_bytes() { return 1024 + kAOBlock + (size_t)kAOStages * kAOStage + sizeof(AOSync); }
 static_assert(kAORanks * kAOHalfPitch * 4 <= kAOStages * kAOStage, "the lower half fits the stages");
+
+// A warp: the NaNs among its stored sums once more, in float32 over the piece's
+// rows: column blocks of 32 (the bits of `blocks`) of a lane's rank j (live:
+// there is one), out its first column.  Ends early where every sum in question is
+// a NaN.  Gradients of 8192 rows, 2048 and 2048 columns, rank 64: 0.4 ms with one
+// infinity in x, 1.5 ms with a row of them, 0.2 ms where x is all NaN (88 us
+// otherwise; looking for NaNs costs 0.2 to 0.4 us).
+__device__ __noinline__ void ao_again(const uint16_t *parts, const uint16_t *z, int D, int cols,
+                                      const int32_t *row, int len, int T, int rp, int j, bool live,
+                                      uint32_t blocks, float *out)
+{
+    for (; blocks; blocks &= blocks - 1) {
+        const int c = (__ffs(blocks) - 1) * 32;
+        uint32_t left = 0;
+        for (int k = 0; k < 32; ++k)
+            if (live && c + k < cols && out[c + k] != out[c + k])
+                left |= 1u << k;
+        float s[32] = {};
+#pragma unroll 1
+        for (int m = 0; m < len; ++m) {
+            const int t = __ldcg(&row[m]);
+            if ((unsigned)t >= (unsigned)T)
+                continue;
+            float u = 0.0f;
+            if (live)
+#pragma unroll
+                for (int i = 0; i < kAdParts; ++i)
+                    u += bf16_to_f32(__ldcg(&parts[((size_t)t * kAdParts + i) * rp + j]));
+#pragma unroll
+            for (int k = 0; k < 32; k += 8)
+                if (c + k < cols) {
+                    const uint4 q = __ldg(reinterpret_cast<const uint4 *>(z + (size_t)t * D + c + k));
+                    s[k] = fmaf(u, bf16lo(q.x), s[k]);
+                    s[k + 1] = fmaf(u, bf16hi(q.x), s[k + 1]);
+                    s[k + 2] = fmaf(u, bf16lo(q.y), s[k + 2]);
+                    s[k + 3] = fmaf(u, bf16hi(q.y), s[k + 3]);
+                    s[k + 4] = fmaf(u, bf16lo(q.z), s[k + 4]);
+                    s[k + 5] = fmaf(u, bf16hi(q.z), s[k + 5]);
+                    s[k + 6] = fmaf(u, bf16lo(q.w), s[k + 6]);
+                    s[k + 7] = fmaf(u, bf16hi(q.w), s[k + 7]);
+                }
+            if ((m & 31) == 31) {
+                bool more = false;
+#pragma unroll
+                for (int k = 0; k < 32; ++k)
+                    more |= (left >> k & 1u) && s[k] == s[k];
+                if (!__any_sync(0xffffffffu, more))
+                    break;
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 32; ++k)
+            if (left >> k & 1u)
+                out[c + k] = s[k];
+    }
+}
 
 __global__ void __launch_bounds__(kAOThreads, 2) k_ad_outer(AdOuterArgs p)
 {
@@ -180,9 +241,10 @@ __global__ void __launch_bounds__(kAOThreads, 2) k_ad_outer(AdOuterArgs p)
     if (warp == kAOWarps) {
         // ------------------------------------------------------------ MMAs
         if (lane == 0) {
-            // both operands along M and N; N in whole sixteens
+            // both operands along M and N; N in whole blocks of the epilogue (the
+            // columns behind the last are zeros)
             const uint32_t idesc =
-                umma_idesc_bf16(128, (cols + 15) & ~15) | (1u << 15) | (1u << 16);
+                umma_idesc_bf16(128, (cols + 31) & ~31) | (1u << 15) | (1u << 16);
             uint32_t acc = 0;
             for (int s = 0; s < ns; ++s) {
                 const int b = s % kAOStages;
@@ -280,6 +342,7 @@ __global__ void __launch_bounds__(kAOThreads, 2) k_ad_outer(AdOuterArgs p)
                         make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
             }
         named_bar_sync(1, kAOWarps * 32);
+        uint32_t again = 0;  // blocks of 32 columns with a NaN
         if (good && quarter < 2 && r0 < ranks)
             for (int c = warp >> 2; c * 32 < cols; c += 2) {
                 float v[32];
@@ -294,9 +357,23 @@ __global__ void __launch_bounds__(kAOThreads, 2) k_ad_outer(AdOuterArgs p)
                     v[j + 2] += h.z;
                     v[j + 3] += h.w;
                 }
+                float bad[4] = {};  // 0 x v: NaN for a NaN (and an infinity)
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    bad[j & 3] = fmaf(v[j], 0.0f, bad[j & 3]);
+                bad[0] += bad[1] + (bad[2] + bad[3]);
+                // (lanes behind the last rank hold nothing)
+                if (__any_sync(0xffffffffu, bad[0] != 0.0f && r0 + lane < ranks))
+                    again |= 1u << c;
                 ag_quad_rows(v);
                 ag_put<float>(out + (size_t)j0 * pr.D + c0, pr.D, c * 32, r0, lane, ranks, cols, v);
             }
+        if (again) {
+            __syncwarp();
+            const AdOuterProblem q = which ? p.pr[1] : p.pr[0];
+            ao_again(q.parts, q.z + c0, q.D, cols, p.row + s_item[1], s_item[2], p.T, ad_rp(p.r),
+                     j0 + r0 + lane, r0 + lane < ranks, again, out + (size_t)(j0 + r0 + lane) * q.D + c0);
+        }
         tc_fence_before();
     }
     __syncthreads();
