@@ -14,7 +14,14 @@
 // tensor cores' running sum loses more at a step than a rounding, so the large
 // sums get one step for 16 rows where all three parts in one would take three
 // (relative error at 8192 rows 8.6e-7 where that gave 1.3e-6; a float32
-// product 7.9e-7); the epilogue adds the halves.
+// product 7.9e-7); the epilogue adds the halves.  What is lost grows with the
+// steps, so one running sum takes kAOSegment stages at most, 48 steps; the sums of
+// a longer piece are added up rounded in its output (dB of 131072 rows in two
+// pieces: 7.7e-5 with one sum each, 7.6e-7 so; a float32 product 1.3e-6).  Pieces
+// are that long beyond about 768 x 256 / (column and rank blocks) rows of one
+// adapter; reading the sums out leaves the tensor cores idle (both gradients of
+// 65536 rows of 4096 and 4096 columns, rank 64, one adapter, eight pieces: 799 us,
+// 627 with one sum each).
 //
 // An infinity in z meets the zeros and, where u has fewer bits, parts of 0:
 // the sums of its column come out NaN.  What came out NaN is computed once more
@@ -60,19 +67,49 @@ constexpr int kAOThreads = (kAOWarps + 1) * 32;
 constexpr int kAOBlock = kAORows * 128;      // 64 values of every row
 constexpr int kAOStage = (kAdParts + kAOCols / 64) * kAOBlock;
 
+constexpr int kAOSegment = 24;  // stages that one tensor-memory sum takes
+
 constexpr int kAOHalfPitch = kAOCols + 4;  // floats of a lower-half row on its way to the upper
 
 struct AOSync {
     uint64_t full[kAOStages];   // every producer's copies of the stage have landed
     uint64_t empty[kAOStages];  // the MMAs reading it have completed
-    uint64_t done;              // every MMA has completed
+    uint64_t done;              // every MMA of the segment has completed
     uint32_t tmem_base;
-    int abort;
+    int abort, stop;            // stop: abort as warp 0 saw it, the same for all warps
 };
 
 // the zeros, the stages (afterwards the lower half's sums), the barriers
 inline size_t ao_smem_bytes() { return 1024 + kAOBlock + (size_t)kAOStages * kAOStage + sizeof(AOSync); }
 static_assert(kAORanks * kAOHalfPitch * 4 <= kAOStages * kAOStage, "the lower half fits the stages");
+
+// Store or add what ag_quad_rows arranged: columns c .. c + 31 of ranks r0 ..
+// r0 + 31.  Whether the warp stored a NaN (or an infinity).
+MOE_DEVINL bool ao_put(float *out, int D, int c, int r0, int lane, int ranks, int cols,
+                       const float (&v)[32], bool add)
+{
+    float bad = 0.0f;  // 0 x v
+#pragma unroll
+    for (int b = 0; b < 32; b += 16)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int row = r0 + (lane & ~3) + k, col = c + (b / 4 + (lane & 3)) * 4;
+            if (row < ranks && col < cols) {
+                float4 *to = reinterpret_cast<float4 *>(out + (size_t)row * D + col);
+                float4 q = make_float4(v[b + 4 * k], v[b + 4 * k + 1], v[b + 4 * k + 2], v[b + 4 * k + 3]);
+                if (add) {
+                    const float4 old = *to;  // this thread's own
+                    q.x += old.x;
+                    q.y += old.y;
+                    q.z += old.z;
+                    q.w += old.w;
+                }
+                *to = q;
+                bad = fmaf(q.x, 0.0f, fmaf(q.y, 0.0f, fmaf(q.z, 0.0f, fmaf(q.w, 0.0f, bad))));
+            }
+        }
+    return __any_sync(0xffffffffu, bad != 0.0f);
+}
 
 // A warp: the NaNs among its stored sums once more, in float32 over the piece's
 // rows: column blocks of 32 (the bits of `blocks`) of a lane's rank j (live:
@@ -241,13 +278,14 @@ __global__ void __launch_bounds__(kAOThreads, 2) k_ad_outer(AdOuterArgs p)
     if (warp == kAOWarps) {
         // ------------------------------------------------------------ MMAs
         if (lane == 0) {
-            // both operands along M and N; N in whole blocks of the epilogue (the
-            // columns behind the last are zeros)
+            // both operands along M and N; N in whole sixteens
             const uint32_t idesc =
-                umma_idesc_bf16(128, (cols + 31) & ~31) | (1u << 15) | (1u << 16);
+                umma_idesc_bf16(128, (cols + 15) & ~15) | (1u << 15) | (1u << 16);
             uint32_t acc = 0;
             for (int s = 0; s < ns; ++s) {
                 const int b = s % kAOStages;
+                if (s % kAOSegment == 0)
+                    acc = 0;
                 if (!mbar_wait(&sy.full[b], (s / kAOStages) & 1, p.status)) {
                     sy.abort = 1;
                     break;
@@ -271,9 +309,12 @@ __global__ void __launch_bounds__(kAOThreads, 2) k_ad_outer(AdOuterArgs p)
                     acc = 1;
                 }
                 umma_commit(&sy.empty[b]);
+                // (its sum is read before the next segment's first stage is full)
+                if ((s + 1) % kAOSegment == 0 && s + 1 < ns)
+                    umma_commit(&sy.done);
             }
             umma_commit(&sy.done);
-            mbar_wait(&sy.done, 0, p.status);
+            mbar_wait(&sy.done, (ns - 1) / kAOSegment & 1, p.status);
         }
         __syncwarp();
     } else {
@@ -293,88 +334,92 @@ __global__ void __launch_bounds__(kAOThreads, 2) k_ad_outer(AdOuterArgs p)
             return lane < kMine && m < len ? __ldg(&p.row[first + m]) : -1;
         };
         int next = ids(0);
-        for (int s = 0; s < ns; ++s) {
-            const int id = next;
-            next = s + 1 < ns ? ids(s + 1) : -1;
-            const int b = s % kAOStages;
+        uint32_t again = 0;  // blocks of 32 columns with a NaN
+        for (int s0 = 0; s0 < ns; s0 += kAOSegment) {
+            for (int s = s0; s < min(ns, s0 + kAOSegment); ++s) {
+                const int id = next;
+                next = s + 1 < ns ? ids(s + 1) : -1;
+                const int b = s % kAOStages;
+                int w = 1;
+                if (lane == 0)
+                    w = mbar_wait(&sy.empty[b], ((s / kAOStages) & 1) ^ 1, p.status);
+                if (!__shfl_sync(0xffffffffu, w, 0)) {
+                    sy.abort = 1;
+                    break;
+                }
+                const uint32_t at = sm + b * kAOStage;
+#pragma unroll
+                for (int i = 0; i < kMine; ++i) {
+                    const int t = __shfl_sync(0xffffffffu, id, i);
+                    const bool live = (unsigned)t < (unsigned)p.T;
+                    const int row = warp + kAOWarps * i;
+                    // zeros for rows behind the piece: they are multiplied too
+                    cp_async16(at + zo + row * 128 + (((lane & 7) ^ (row & 7)) << 4),
+                               live && zl ? zp + (size_t)t * pr.D : pr.z, live && zl);
+                    if (pl)
+                        cp_async16(at + part * kAOBlock + row * 128 + ((ch ^ (row & 7)) << 4),
+                                   live ? up + (size_t)t * kAdParts * rp : pr.parts, live);
+                }
+                cp_async_arrive(&sy.full[b]);
+            }
+            cp_async_wait<0>();
+            // -------------------------------------------------------- epilogue
+            // warps 2, 3, 6, 7 hold the lower half of tensor memory's lanes and hand
+            // their sums over; warps 0, 1, 4, 5 add them and store
             int w = 1;
             if (lane == 0)
-                w = mbar_wait(&sy.empty[b], ((s / kAOStages) & 1) ^ 1, p.status);
-            if (!__shfl_sync(0xffffffffu, w, 0)) {
-                sy.abort = 1;
-                break;
-            }
-            const uint32_t at = sm + b * kAOStage;
+                w = mbar_wait(&sy.done, s0 / kAOSegment & 1, p.status);
+            const bool good = __shfl_sync(0xffffffffu, w, 0) && !*(volatile int *)&sy.abort;
+            tc_fence_after();
+            const int quarter = warp & 3, r0 = (quarter & 1) * 32;  // first rank of this warp's lanes
+            const uint32_t from = tmem + ((uint32_t)(quarter * 32) << 16);
+            float *half = reinterpret_cast<float *>(ring);
+            if (good && quarter >= 2 && r0 < ranks)
+                for (int c = warp >> 2; c * 32 < cols; c += 2) {
+                    float v[32];
+                    __syncwarp();
+                    tmem_ld32(from + c * 32, v);
 #pragma unroll
-            for (int i = 0; i < kMine; ++i) {
-                const int t = __shfl_sync(0xffffffffu, id, i);
-                const bool live = (unsigned)t < (unsigned)p.T;
-                const int row = warp + kAOWarps * i;
-                // zeros for rows behind the piece: they are multiplied too
-                cp_async16(at + zo + row * 128 + (((lane & 7) ^ (row & 7)) << 4),
-                           live && zl ? zp + (size_t)t * pr.D : pr.z, live && zl);
-                if (pl)
-                    cp_async16(at + part * kAOBlock + row * 128 + ((ch ^ (row & 7)) << 4),
-                               live ? up + (size_t)t * kAdParts * rp : pr.parts, live);
-            }
-            cp_async_arrive(&sy.full[b]);
-        }
-        cp_async_wait<0>();
-        // ------------------------------------------------------------ epilogue
-        // warps 2, 3, 6, 7 hold the lower half of tensor memory's lanes and hand
-        // their sums over; warps 0, 1, 4, 5 add them and store
-        int w = 1;
-        if (lane == 0)
-            w = mbar_wait(&sy.done, 0, p.status);
-        const bool good = __shfl_sync(0xffffffffu, w, 0) && !*(volatile int *)&sy.abort;
-        tc_fence_after();
-        const int quarter = warp & 3, r0 = (quarter & 1) * 32;  // first rank of this warp's lanes
-        const uint32_t from = tmem + ((uint32_t)(quarter * 32) << 16);
-        float *half = reinterpret_cast<float *>(ring);
-        if (good && quarter >= 2 && r0 < ranks)
-            for (int c = warp >> 2; c * 32 < cols; c += 2) {
-                float v[32];
-                __syncwarp();
-                tmem_ld32(from + c * 32, v);
-#pragma unroll
-                for (int j = 0; j < 32; j += 4)
-                    *reinterpret_cast<float4 *>(half + (r0 + lane) * kAOHalfPitch + c * 32 + j) =
-                        make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
-            }
-        named_bar_sync(1, kAOWarps * 32);
-        uint32_t again = 0;  // blocks of 32 columns with a NaN
-        if (good && quarter < 2 && r0 < ranks)
-            for (int c = warp >> 2; c * 32 < cols; c += 2) {
-                float v[32];
-                __syncwarp();
-                tmem_ld32(from + c * 32, v);
-#pragma unroll
-                for (int j = 0; j < 32; j += 4) {
-                    const float4 h = *reinterpret_cast<const float4 *>(
-                        half + (r0 + lane) * kAOHalfPitch + c * 32 + j);
-                    v[j] += h.x;
-                    v[j + 1] += h.y;
-                    v[j + 2] += h.z;
-                    v[j + 3] += h.w;
+                    for (int j = 0; j < 32; j += 4)
+                        *reinterpret_cast<float4 *>(half + (r0 + lane) * kAOHalfPitch + c * 32 + j) =
+                            make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
                 }
-                float bad[4] = {};  // 0 x v: NaN for a NaN (and an infinity)
+            named_bar_sync(1, kAOWarps * 32);
+            if (good && quarter < 2 && r0 < ranks)
+                for (int c = warp >> 2; c * 32 < cols; c += 2) {
+                    float v[32];
+                    __syncwarp();
+                    tmem_ld32(from + c * 32, v);
 #pragma unroll
-                for (int j = 0; j < 32; ++j)
-                    bad[j & 3] = fmaf(v[j], 0.0f, bad[j & 3]);
-                bad[0] += bad[1] + (bad[2] + bad[3]);
-                // (lanes behind the last rank hold nothing)
-                if (__any_sync(0xffffffffu, bad[0] != 0.0f && r0 + lane < ranks))
-                    again |= 1u << c;
-                ag_quad_rows(v);
-                ag_put<float>(out + (size_t)j0 * pr.D + c0, pr.D, c * 32, r0, lane, ranks, cols, v);
+                    for (int j = 0; j < 32; j += 4) {
+                        const float4 h = *reinterpret_cast<const float4 *>(
+                            half + (r0 + lane) * kAOHalfPitch + c * 32 + j);
+                        v[j] += h.x;
+                        v[j + 1] += h.y;
+                        v[j + 2] += h.z;
+                        v[j + 3] += h.w;
+                    }
+                    ag_quad_rows(v);
+                    if (ao_put(out + (size_t)j0 * pr.D + c0, pr.D, c * 32, r0, lane, ranks, cols, v,
+                               s0 > 0))
+                        again |= 1u << c;
+                }
+            tc_fence_before();
+            if (s0 + kAOSegment < ns) {
+                if (tid == 0)
+                    sy.stop = *(volatile int *)&sy.abort;
+                named_bar_sync(1, kAOWarps * 32);  // the lower half has been read
+                if (*(volatile int *)&sy.stop)
+                    break;
             }
+        }
         if (again) {
             __syncwarp();
             const AdOuterProblem q = which ? p.pr[1] : p.pr[0];
+            const int r0 = (warp & 1) * 32;
             ao_again(q.parts, q.z + c0, q.D, cols, p.row + s_item[1], s_item[2], p.T, ad_rp(p.r),
                      j0 + r0 + lane, r0 + lane < ranks, again, out + (size_t)(j0 + r0 + lane) * q.D + c0);
         }
-        tc_fence_before();
     }
     __syncthreads();
     if (warp == kAOWarps) {
