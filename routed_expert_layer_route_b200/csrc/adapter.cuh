@@ -41,10 +41,13 @@ MOE_DEVINL int adapter_of(const int32_t *adapter, int t, int n, int *status)
 constexpr int kAdParts = 3;
 constexpr int kAdMaxR = 128;  // ranks
 
-// The parts of u; a value beyond the finite numbers is all in the first.
+// The parts of u; a value beyond the finite numbers is all in the first, and a
+// finite one that would round to an infinity has the largest bf16 there.
 MOE_DEVINL void split_bf16(float v, uint16_t (&part)[kAdParts])
 {
     part[0] = f32_to_bf16_rn(v);
+    if ((part[0] & 0x7fffu) == 0x7f80u && fabsf(v) < __int_as_float(0x7f800000))
+        part[0] -= 1;
     const bool finite = (part[0] & 0x7f80u) != 0x7f80u;
 #pragma unroll
     for (int i = 1; i < kAdParts; ++i) {

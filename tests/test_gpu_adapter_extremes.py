@@ -60,3 +60,39 @@ def test_infinities_in_gradients(T, din, dout, r, n):
     calm = [torch.where(torch.isfinite(t), t, torch.zeros_like(t)) for t in (u, dy)]
     check_with_infinities(d_lora_b(c, u, dy), want, ref.outer(*calm, c.adapter, n)[1], "d_lora_b")
     assert moe.moe_read_device_status(ws) == 0
+
+
+@pytest.mark.parametrize("T", [5, 600, 2500, 4500])
+def test_the_largest_numbers_of_u(T):
+    # above the largest bf16: the first part may not become an infinity
+    c = ref.Case(T, 64, 72, 6, 2, "one", seed=37)
+    u = torch.zeros(T, 6, device=DEV)
+    top = torch.finfo(torch.float32).max
+    u[1, 0], u[2, 1], u[3, 5] = top, -top, 3.3953e38
+    dy = torch.zeros(T, 72, device=DEV, dtype=torch.bfloat16)
+    dy[1, 3], dy[2, 7], dy[3, 71], dy[1, 64] = 0.5, 0.25, -0.5, 0.0
+    db = d_lora_b(c, u, dy)
+    want = (u.double().t() @ dy.double())[None]
+    assert torch.isfinite(db).all()
+    assert float((db[1].double() - want[0]).abs().max()) <= 2.0 ** -22 * top
+    assert (db[1][want[0] == 0] == 0).all() and (db[0] == 0).all()
+
+
+@pytest.mark.parametrize("T", [20, 100, 2500, 5000])
+def test_the_largest_numbers_of_the_projection(T):
+    # u itself above the largest bf16: one product of the inner sum, the rest zeros
+    n, r, d = 2, 5, 72
+    c = ref.Case(T, d, d, r, n, "one", seed=38)
+    for t in (c.x, c.a, c.b):
+        t.zero_()
+    big = 2.0 ** 64 * (1 - 2.0 ** -8)
+    c.x[3, 8], c.a[1, 2, 8] = big, big          # u = 2^128 (1 - 2^-8)^2 = 2^128 (1 - 2^-7 + 2^-16)
+    c.x[7, 9], c.a[1, 4, 9] = -(2.0 ** 64 - 2.0 ** 56), 2.0 ** 63
+    c.b[1, 2, 3], c.b[1, 4, 5] = 0.5, 1.0
+    scale = torch.tensor([1.0, 1.0 + 2.0 ** -7 - 2.0 ** -12], device=DEV)
+    wu = scale[1].double() * (c.x.double() @ c.a[1].double().t())
+    y, u = torch.zeros(T, d, device=DEV), torch.empty(T, r, device=DEV)
+    moe.moe_adapter_linear(c.x, None, None, c.adapter, c.a, c.b, scale, y, c.workspace(), u_out=u)
+    assert float(wu.abs().max()) > 3.397e38 and torch.isfinite(u).all()
+    assert torch.allclose(u.double(), wu, rtol=2.0 ** -22, atol=0.0)
+    assert torch.allclose(y.double(), wu @ c.b[1].double(), rtol=2.0 ** -22, atol=0.0)
