@@ -428,6 +428,13 @@ def _given(where, device, *tensors):
     return pointers
 
 
+def _given_ws(where, device, ws):
+    """_ws_args of a workspace that is dense and on the current device."""
+    if ws is not None and not (ws.is_contiguous() and ws.get_device() == device):
+        raise MoeError(MOE_ERR_INVALID_ARG, where)
+    return _ws_args(ws)
+
+
 def _out_dtype(t):
     return MOE_DTYPE_BF16 if t is not None and t.dtype == torch.bfloat16 else MOE_DTYPE_F32
 
@@ -453,12 +460,13 @@ def moe_adapter_linear(x, w, bias, adapter, lora_a, lora_b, scale, y, ws, u_out=
     w None: the adapters' part is added to y."""
     T, din = x.shape
     n, r, dout = lora_b.shape
+    device = torch.cuda.current_device()
     *inputs, yp, up = _given(
-        "moe_adapter_linear", torch.cuda.current_device(), (x, _BF16, (T, din)),
+        "moe_adapter_linear", device, (x, _BF16, (T, din)),
         (w, _BF16, (dout, din)), (bias, _F32, (dout,)), (adapter, _I32, (T,)),
         (lora_a, _BF16, (n, r, din)), (lora_b, _BF16, (n, r, dout)), (scale, _F32, (n,)),
         (y, _OUT, (T, dout)), (u_out, _F32, (T, r)))
-    wsp, wsn = _ws_args(ws)
+    wsp, wsn = _given_ws("moe_adapter_linear", device, ws)
     _check(lib().moe_adapter_linear(*inputs, T, din, dout, r, n, yp, _out_dtype(y), up, wsp, wsn,
                                     _stream(stream)), "moe_adapter_linear")
 
@@ -470,13 +478,14 @@ def moe_adapter_backward(dy, x, w_t, adapter, lora_a, lora_b, scale, u, d_lora_a
     u as moe_adapter_linear's u_out."""
     T, dout = dy.shape
     n, r, din = lora_a.shape
+    device = torch.cuda.current_device()
     *inputs, dap, dbp, dxp = _given(
-        "moe_adapter_backward", torch.cuda.current_device(), (dy, _BF16, (T, dout)),
+        "moe_adapter_backward", device, (dy, _BF16, (T, dout)),
         (x, _BF16, (T, din)), (w_t, _BF16, (din, dout)), (adapter, _I32, (T,)),
         (lora_a, _BF16, (n, r, din)), (lora_b, _BF16, (n, r, dout)), (scale, _F32, (n,)),
         (u, _F32, (T, r)), (d_lora_a, _F32, (n, r, din)), (d_lora_b, _F32, (n, r, dout)),
         (dx, _OUT, (T, din)))
-    wsp, wsn = _ws_args(ws)
+    wsp, wsn = _given_ws("moe_adapter_backward", device, ws)
     _check(lib().moe_adapter_backward(*inputs, T, din, dout, r, n, dxp, _out_dtype(dx), dap, dbp, wsp,
                                       wsn, _stream(stream)), "moe_adapter_backward")
 
@@ -503,11 +512,12 @@ def moe_balance_loss(logits, topk_idx, balance_coef, z_coef, counts, loss, ws, t
     token_mask [T] bool or uint8, False for padding."""
     T, E = logits.shape
     k1 = topk_idx.shape[-1]
+    device = torch.cuda.current_device()
     *inputs, counts, loss, prob_mean = _given(
-        "moe_balance_loss", torch.cuda.current_device(), (logits, _F32, (T, E)),
+        "moe_balance_loss", device, (logits, _F32, (T, E)),
         (topk_idx, _I32, (T, k1)), (token_mask, _BYTE, (T,)), (counts, _I32, (E + 1,)),
         (loss, _F32, (3,)), (prob_mean, _F32, (E,)))
-    wsp, wsn = _ws_args(ws)
+    wsp, wsn = _given_ws("moe_balance_loss", device, ws)
     _check(lib().moe_balance_loss(*inputs, T, E, k1, float(balance_coef), float(z_coef), counts, loss,
                                   prob_mean, wsp, wsn, _stream(stream)), "moe_balance_loss")
 
@@ -519,13 +529,14 @@ def moe_route_backward(logits, topk_idx, k2, d_topk_w, dlogits, counts=None, bal
     float32 scalar, None for 1)."""
     T, E = logits.shape
     k1 = topk_idx.shape[-1]
+    device = torch.cuda.current_device()
     *inputs, d_loss, dzp = _given(
-        "moe_route_backward", torch.cuda.current_device(), (logits, _F32, (T, E)),
+        "moe_route_backward", device, (logits, _F32, (T, E)),
         (topk_idx, _I32, (T, k1)), (d_topk_w, _F32, (T, k1)), (counts, _I32, (E + 1,)),
         (token_mask, _BYTE, (T,)),
         (d_loss, _F32, d_loss.shape if d_loss is not None and d_loss.numel() == 1 else None),
         (dlogits, _OUT, (T, E)))
-    wsp, wsn = _ws_args(ws)
+    wsp, wsn = _given_ws("moe_route_backward", device, ws)
     _check(lib().moe_route_backward(*inputs, T, E, k1, k2, float(balance_coef), float(z_coef), d_loss,
                                     dzp, _out_dtype(dlogits), wsp, wsn, _stream(stream)),
            "moe_route_backward")
