@@ -17,6 +17,7 @@ from routed_expert_layer_route_b200 import moe
 pytestmark = pytest.mark.gpu
 DEV = torch.device("cuda:0")
 SEGMENT = 48  # most steps of one sum of a float32 output
+PARTS = 12    # of an adapter's part: three parts of u for each 16 of 64 ranks
 
 
 def norm_bound(steps):
@@ -25,6 +26,39 @@ def norm_bound(steps):
 
 def far(got, want):
     return float((got.double() - want).norm() / want.norm())
+
+
+def by_rows(u, b, adapter, n):
+    """The adapters' part of y from given u, in 64 bits."""
+    y = torch.zeros(u.shape[0], b.shape[2], dtype=torch.float64, device=DEV)
+    for i in range(n):
+        t = (adapter == i).nonzero()[:, 0]
+        y[t] = u[t].double() @ b[i].double()
+    return y
+
+
+@pytest.mark.parametrize("T,din,dout,r,n,rows", [
+    (1100, 8192, 1032, 16, 4, "runs"), (2600, 4096, 2056, 24, 3, "runs"), (100, 8192, 264, 40, 6, "mixed"),
+    (300, 4104, 136, 16, 3, "mixed"), (40, 4096, 136, 16, 4, "mixed")], ids=str)
+def test_projection_of_a_long_k(T, din, dout, r, n, rows):
+    c = ref.Case(T, din, dout, r, n, rows, seed=31)
+    y, u = torch.empty(T, dout, device=DEV), torch.empty(T, r, device=DEV)
+    ws = c.workspace()
+    moe.moe_adapter_linear(c.x, c.w, c.bias, c.adapter, c.a, c.b, c.scale, y, ws, u_out=u)
+    want = c.x.double() @ c.w.double().t() + c.bias.double() + by_rows(u, c.b, c.adapter, n)
+    assert far(y, want) <= norm_bound(SEGMENT)
+    # the inner products: K is split over four warps at least
+    assert far(u, ref.inner(c.x, c.a, c.adapter, c.scale)[0]) <= norm_bound((din // 4 + 15) // 16)
+    assert moe.moe_read_device_status(ws) == 0
+
+
+@pytest.mark.parametrize("T,dout,r,n", [(2600, 2056, 64, 3), (500, 264, 33, 4), (50, 264, 64, 3)], ids=str)
+def test_the_adapters_part_alone(T, dout, r, n):
+    # u with 24 bits
+    c = ref.Case(T, 128, dout, r, n, "runs", seed=32)
+    y, u = torch.zeros(T, dout, device=DEV), torch.empty(T, r, device=DEV)
+    moe.moe_adapter_linear(c.x, None, None, c.adapter, c.a, c.b, c.scale, y, c.workspace(), u_out=u)
+    assert far(y, by_rows(u, c.b, c.adapter, n)) <= norm_bound(PARTS)
 
 
 def d_lora_b(c, u, dy):
@@ -85,3 +119,22 @@ def test_infinities_in_long_sums(row):
     assert torch.equal(torch.isnan(got), torch.isnan(want))
     assert torch.equal(got[torch.isinf(want)].double(), want[torch.isinf(want)])
     assert far(got[fine], want[fine]) <= norm_bound(SEGMENT)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("shape", [(2600, 1032, 2056, 24, 3, "runs"), (2600, 1032, 2056, 16, 9, "mixed"),
+                                   (5000, 520, 1032, 40, 4, "mixed")], ids=str)
+def test_more_tiles_than_pairs_with_a_long_k(shape, dtype):
+    # the K ring turns within a tile, segments and units of adapters follow each other over tiles
+    c = ref.Case(*shape, seed=35)
+    y, u = torch.empty(c.T, c.dout, device=DEV, dtype=dtype), torch.empty(c.T, c.r, device=DEV)
+    ws = c.workspace()
+    moe.moe_adapter_linear(c.x, c.w, c.bias, c.adapter, c.a, c.b, c.scale, y, ws, u_out=u)
+    want, e, wu, eu = ref.linear(c.x, c.w, c.bias, c.adapter, c.a, c.b, c.scale)
+    ref.check(y, want, e, "y")
+    ref.check(u, wu, eu, "u")
+    for _ in range(3):
+        again = torch.empty_like(y)
+        moe.moe_adapter_linear(c.x, c.w, c.bias, c.adapter, c.a, c.b, c.scale, again, ws)
+        assert torch.equal(again, y)
+    assert moe.moe_read_device_status(ws) == 0
