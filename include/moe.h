@@ -405,16 +405,20 @@ int moe_adapter_backward(const void *dy_bf16, const void *x_bf16, const void *w_
  *     L_z = (1/N) sum_t lse_t^2
  *   counts [E + 1] int32: n_e, and N behind them; loss [3] float32:
  *   balance_coef L_bal + z_coef L_z, L_bal, L_z; prob_mean [E] float32
- *   (nullable): P_e.  N = 0 gives zeros.  NaN or +inf logits in a counting
- *   row make losses and P_e NaN.  ws: moe_balance_workspace_size bytes,
- *   initialised with moe_workspace_init.
+ *   (nullable): P_e.  Sums of p_te are kept in steps of 2^-40: P_e is off by
+ *   at most 2^-31 / N beside its float32 rounding, and 0 for an expert whose
+ *   probabilities are all far below 2^-40.  N = 0 gives zeros.
+ *   NaN or +inf logits in a counting row make losses and P_e NaN.  ws:
+ *   moe_balance_workspace_size bytes, initialised with moe_workspace_init.
  * moe_route_backward: dlogits [T x E] of dz_dtype (MOE_DTYPE_*, rounded
  *   once), the sum of two parts, each left out when its input is NULL:
  *   - d_topk_w [T x k1] float32, the gradient of the Eq. 2 weights: with K2
  *     the row's given experts and, of the others, those of the largest
  *     logits (equal ones by the lower index), min(k2, E) in all, and w the
  *     softmax over K2, dz_m = w_m (g_m - sum_i g_i w_i) in K2, 0 elsewhere.
- *     Entries of empty slots are not used.
+ *     Entries of empty slots are not used.  Where the weights are those of
+ *     moe_combine, d_topk_w[t, s] = <dy[t], expert_out[slot_pos[t*k1+s]]>
+ *     with moe_expert_ffn's expert_out.
  *   - counts [E + 1] from moe_balance_loss (or summed over several batches
  *     or ranks): the gradient of balance_coef L_bal + z_coef L_z, the counts
  *     held fixed, times d_loss (device float32 scalar, NULL: 1).
