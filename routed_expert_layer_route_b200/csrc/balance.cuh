@@ -21,7 +21,11 @@
 // T = 65536, E = 512: k_balance 28 us, 4.9 TB/s, bound by the read (76% of the
 // copy bandwidth); k_route_backward with both parts, k1 = 5, k2 = 20, 85 us,
 // bound by its instructions (about 950 a row, 400 of them on the half-rate
-// comparison and logic pipe; reading and writing alone would take 32 us).
+// comparison and logic pipe; reading and writing alone would take 32 us).  Rows
+// with equal logits on the border take the general row, which raises the tied
+// experts one by one: the weights' part alone takes 74 us for logits without ties,
+// 411 us for logits in steps of 1/4, 231 us for equal ones (a new router's), and
+// for 4096 rows of 1024 experts, k2 = 1023, 17 us and 1.1 ms.
 // Small calls take 4 to 5 us, a launch and one pass of dependent loads.
 #pragma once
 #include "common.cuh"

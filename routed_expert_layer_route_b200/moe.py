@@ -429,10 +429,12 @@ def _given(where, device, *tensors):
 
 
 def _given_ws(where, device, ws):
-    """_ws_args of a workspace that is dense and on the current device."""
-    if ws is not None and not (ws.is_contiguous() and ws.get_device() == device):
-        raise MoeError(MOE_ERR_INVALID_ARG, where)
-    return _ws_args(ws)
+    """_ws_args of a workspace that has to be dense and on the current device."""
+    if ws is None:
+        return None, 0
+    if ws.is_contiguous() and ws.get_device() == device:
+        return ws.data_ptr(), ws.nbytes
+    raise MoeError(MOE_ERR_INVALID_ARG, where)
 
 
 def _out_dtype(t):
