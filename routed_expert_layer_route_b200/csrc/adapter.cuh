@@ -69,6 +69,14 @@ MOE_DEVINL void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, u
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// The matrix instructions' running sum rounds towards zero at each step of 16
+// products, so what it loses grows with K.  One sum takes kAdSteps of them at most;
+// the sums of a longer K are added up rounded.  u of 2500 rows at K = 4096 and 16384:
+// 2.4e-7 off 64 bits, where sums of any length had 1.0e-6 and 4.4e-6 and a float32
+// product has 1.5e-7 and 3.2e-7; 8192 rows of 4096, rank 32, take 2 us more with it
+// (48 steps: 1 us, 7e-7).
+constexpr int kAdSteps = 16;
+
 MOE_DEVINL void cp_async16(uint32_t dst, const void *src, bool live)
 {
     const int n = live ? 16 : 0;  // 0: zeros
@@ -342,49 +350,54 @@ __global__ void __launch_bounds__(kAdWarps * 32, NT >= 8 ? 1 : 2) k_ad_inner(AdI
     }
     for (int l = part; l < count; l += p.lists) {
         const int a = s_list[l];
-        float acc[MT][NT][4];
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int i = 0; i < NT; ++i)
-                acc[m][i][0] = acc[m][i][1] = acc[m][i][2] = acc[m][i][3] = 0.0f;
         const uint16_t *ap = p.a + ((size_t)a * p.r + j0 + g) * p.din;
+        constexpr int kSegment = kAdWarps * kAdSteps / 2;  // chunks of one running sum of every warp
+        for (int s0 = 0; s0 < nc; s0 += kSegment) {
+            float acc[MT][NT][4];
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int i = 0; i < NT; ++i)
+                    acc[m][i][0] = acc[m][i][1] = acc[m][i][2] = acc[m][i][3] = 0.0f;
+            const int s1 = min(nc, s0 + kSegment);
 #pragma unroll(NT <= 2 ? 8 : 4)
-        for (int c = warp; c < nc; c += kAdWarps) {
-            const int k = c * kAdChunk + 8 * q;
-            uint4 u[2 * MT];
-#pragma unroll
-            for (int m = 0; m < 2 * MT; ++m)
-                u[m] = ad_chunk(xr[m], k, p.din, has[m]);
-#pragma unroll
-            for (int i = 0; i < NT; ++i) {
-                const uint4 w = ad_chunk(ap + (size_t)i * 8 * p.din, k, p.din,
-                                         j0 + 8 * i + g < p.r);
-#pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    mma_bf16(acc[m][i], u[2 * m].x, u[2 * m + 1].x, u[2 * m].y, u[2 * m + 1].y, w.x,
-                             w.y);
-                    mma_bf16(acc[m][i], u[2 * m].z, u[2 * m + 1].z, u[2 * m].w, u[2 * m + 1].w, w.z,
-                             w.w);
-                }
-            }
-        }
-        // the upper warps' sums of this adapter's rows, then the lower ones' added
-#pragma unroll
-        for (int half = 1; half >= 0; --half) {
-            if (warp / (kAdWarps / 2) == half)
+            for (int c = s0 + warp; c < s1; c += kAdWarps) {
+                const int k = c * kAdChunk + 8 * q;
+                uint4 u[2 * MT];
 #pragma unroll
                 for (int m = 0; m < 2 * MT; ++m)
-                    if (sa[8 * m + g] == a)
+                    u[m] = ad_chunk(xr[m], k, p.din, has[m]);
 #pragma unroll
-                        for (int i = 0; i < NT; ++i)
+                for (int i = 0; i < NT; ++i) {
+                    const uint4 w = ad_chunk(ap + (size_t)i * 8 * p.din, k, p.din,
+                                             j0 + 8 * i + g < p.r);
 #pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                float &to = red[warp % (kAdWarps / 2)][8 * m + g][8 * i + 2 * q + h];
-                                const float v = acc[m / 2][i][2 * (m & 1) + h];
-                                to = half ? v : to + v;
-                            }
-            __syncthreads();
+                    for (int m = 0; m < MT; ++m) {
+                        mma_bf16(acc[m][i], u[2 * m].x, u[2 * m + 1].x, u[2 * m].y, u[2 * m + 1].y,
+                                 w.x, w.y);
+                        mma_bf16(acc[m][i], u[2 * m].z, u[2 * m + 1].z, u[2 * m].w, u[2 * m + 1].w,
+                                 w.z, w.w);
+                    }
+                }
+            }
+            // the upper warps' sums of this adapter's rows, then the lower ones' added
+#pragma unroll
+            for (int half = 1; half >= 0; --half) {
+                if (warp / (kAdWarps / 2) == half)
+#pragma unroll
+                    for (int m = 0; m < 2 * MT; ++m)
+                        if (sa[8 * m + g] == a)
+#pragma unroll
+                            for (int i = 0; i < NT; ++i)
+#pragma unroll
+                                for (int h = 0; h < 2; ++h) {
+                                    float &to =
+                                        red[warp % (kAdWarps / 2)][8 * m + g][8 * i + 2 * q + h];
+                                    const float v = acc[m / 2][i][2 * (m & 1) + h];
+                                    to = half && s0 == 0 ? v : to + v;
+                                }
+                __syncthreads();
+            }
         }
     }
     // the rows of this CTA's adapters (part 0: those without one too)
@@ -436,6 +449,17 @@ struct AdBigShape {
     static constexpr int kRedPitch = 8 * NT + 1;  // the halves' sums, in the stages' place
 };
 
+// An array that is to lie in local memory: the registers are the main loop's (64
+// with two CTAs an SM; with 16 more values among them 8192 rows of 2048, rank 64,
+// take 7 us more).
+template <int N>
+MOE_DEVINL float *ad_local(float (&v)[N])
+{
+    float *p = v;
+    asm volatile("" : "+l"(p)::"memory");
+    return p;
+}
+
 template <int NT>
 __global__ void __launch_bounds__(kAdBigWarps * 32) k_ad_inner_big(AdInnerArgs p)
 {
@@ -470,6 +494,7 @@ __global__ void __launch_bounds__(kAdBigWarps * 32) k_ad_inner_big(AdInnerArgs p
     const int ns = (p.din + S::kK - 1) / S::kK;
     constexpr int kMT = R / 16, kKG = kAdBigWarps / (2 * kMT);  // row tiles, parts of a stage
     constexpr int NH = NT / 2, KS = S::kK / 16 / kKG;           // instructions of N and of K
+    constexpr int kSegment = kAdSteps / KS;                     // stages of one running sum
     const int mt = warp % kMT, nh = warp / kMT % 2, kh = warp / (2 * kMT);
     // this thread's vectors of a stage: column ck of row tid / 16 of x, then of
     // ranks tid / 16, + 32 of the adapter; nullptr: zeros
@@ -500,6 +525,7 @@ __global__ void __launch_bounds__(kAdBigWarps * 32) k_ad_inner_big(AdInnerArgs p
             cp_async_commit();
         };
         float acc[NH][4];
+        float done[NH * 4];  // sums of the segments before: in local memory, seldom used
 #pragma unroll
         for (int i = 0; i < NH; ++i)
             acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.0f;
@@ -507,41 +533,62 @@ __global__ void __launch_bounds__(kAdBigWarps * 32) k_ad_inner_big(AdInnerArgs p
 #pragma unroll
         for (int s = 0; s < S::kStages - 1; ++s)
             issue(s);
-        for (int s = 0; s < ns; ++s) {
-            cp_async_wait<S::kStages - 2>();
-            __syncthreads();
-            issue(s + S::kStages - 1);
-            const uint32_t at = sm + (s % S::kStages) * S::kStage + kh * KS * 32;
-            uint32_t x[KS][4], w[KS][NH == 1 ? 1 : NH / 2][4];
+        for (int s0 = 0; s0 < ns; s0 += kSegment) {
+            const int s1 = min(ns, s0 + kSegment);
+            for (int s = s0; s < s1; ++s) {
+                cp_async_wait<S::kStages - 2>();
+                __syncthreads();
+                issue(s + S::kStages - 1);
+                const uint32_t at = sm + (s % S::kStages) * S::kStage + kh * KS * 32;
+                uint32_t x[KS][4], w[KS][NH == 1 ? 1 : NH / 2][4];
 #pragma unroll
-            for (int kk = 0; kk < KS; ++kk) {
-                ldmatrix_x4(at + (mt * 16 + (lane & 15)) * S::kPitch + kk * 32 + (lane >> 4) * 16,
-                            x[kk]);
-                if (NH == 1) {
-                    const uint32_t addr = at + (S::kRows + nh * 8 + (lane & 7)) * S::kPitch +
-                                          kk * 32 + ((lane >> 3) & 1) * 16;
-                    asm volatile("ldmatrix.sync.aligned.m8n8.x2.shared.b16 {%0,%1}, [%2];"
-                                 : "=r"(w[kk][0][0]), "=r"(w[kk][0][1])
-                                 : "r"(addr)
-                                 : "memory");
-                } else {
+                for (int kk = 0; kk < KS; ++kk) {
+                    ldmatrix_x4(at + (mt * 16 + (lane & 15)) * S::kPitch + kk * 32 + (lane >> 4) * 16,
+                                x[kk]);
+                    if (NH == 1) {
+                        const uint32_t addr = at + (S::kRows + nh * 8 + (lane & 7)) * S::kPitch +
+                                              kk * 32 + ((lane >> 3) & 1) * 16;
+                        asm volatile("ldmatrix.sync.aligned.m8n8.x2.shared.b16 {%0,%1}, [%2];"
+                                     : "=r"(w[kk][0][0]), "=r"(w[kk][0][1])
+                                     : "r"(addr)
+                                     : "memory");
+                    } else {
 #pragma unroll
-                    for (int i = 0; i < NH / 2; ++i)  // two blocks of eight ranks
-                        ldmatrix_x4(at + (S::kRows + nh * 8 * NH + i * 16 + (lane & 7) +
-                                          (lane >> 4) * 8) * S::kPitch +
-                                        kk * 32 + ((lane >> 3) & 1) * 16,
-                                    w[kk][i]);
+                        for (int i = 0; i < NH / 2; ++i)  // two blocks of eight ranks
+                            ldmatrix_x4(at + (S::kRows + nh * 8 * NH + i * 16 + (lane & 7) +
+                                              (lane >> 4) * 8) * S::kPitch +
+                                            kk * 32 + ((lane >> 3) & 1) * 16,
+                                        w[kk][i]);
+                    }
                 }
-            }
 #pragma unroll
-            for (int kk = 0; kk < KS; ++kk)
+                for (int kk = 0; kk < KS; ++kk)
+#pragma unroll
+                    for (int i = 0; i < NH; ++i)
+                        mma_bf16(acc[i], x[kk][0], x[kk][1], x[kk][2], x[kk][3], w[kk][i / 2][2 * (i & 1)],
+                                 w[kk][i / 2][2 * (i & 1) + 1]);
+            }
+            if (s1 < ns) {  // sums of a segment, added rounded
+                float *to = ad_local(done);
 #pragma unroll
                 for (int i = 0; i < NH; ++i)
-                    mma_bf16(acc[i], x[kk][0], x[kk][1], x[kk][2], x[kk][3], w[kk][i / 2][2 * (i & 1)],
-                             w[kk][i / 2][2 * (i & 1) + 1]);
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) {
+                        to[i * 4 + h] = s0 == 0 ? acc[i][h] : to[i * 4 + h] + acc[i][h];
+                        acc[i][h] = 0.0f;
+                    }
+            }
         }
         cp_async_wait<0>();
         __syncthreads();
+        if (ns > kSegment) {
+            const float *from = ad_local(done);
+#pragma unroll
+            for (int i = 0; i < NH; ++i)
+#pragma unroll
+                for (int h = 0; h < 4; ++h)
+                    acc[i][h] += from[i * 4 + h];
+        }
         // the parts of K meet
         if (kh > 0) {
             float *mine = red + (kh - 1) * R * S::kRedPitch;
@@ -663,6 +710,7 @@ template <int NT>
 struct AdRowsShape {
     static constexpr int kDeep = NT <= 4 ? 8 : 4;              // chunks of a warp in a phase
     static constexpr int kPhase = kDeep * kAdWarps * kAdChunk;  // values of K
+    static_assert(2 * kDeep <= kAdSteps, "a phase is one running sum");
     static constexpr int kPitch = kPhase * 2 + 64;  // bytes; 64 over: two rows on other banks
     static constexpr int kX = 8 * NT * kPitch;
     static constexpr int kRed = kAdWarps * 8 * NT * 17 * 4;
@@ -752,10 +800,12 @@ __global__ void __launch_bounds__(kAdWarps * 32) k_ad_rows(AdProductArgs p, AdOn
             }
         }
     }
-    float acc[NT][4];
+    float acc[NT][4], sum[NT][4];
 #pragma unroll
     for (int i = 0; i < NT; ++i)
-        acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.0f;
+#pragma unroll
+        for (int h = 0; h < 4; ++h)
+            acc[i][h] = sum[i][h] = 0.0f;
     for (int k0 = 0; k0 < K; k0 += S::kPhase) {
         cp_async_wait<0>();
         __syncthreads();
@@ -773,9 +823,22 @@ __global__ void __launch_bounds__(kAdWarps * 32) k_ad_rows(AdProductArgs p, AdOn
             }
         }
         __syncthreads();
-        if (k0 + S::kPhase < K)
+        if (k0 + S::kPhase < K) {
             fetch(k0 + S::kPhase);
+#pragma unroll
+            for (int i = 0; i < NT; ++i)  // a phase's sums (kAdSteps at most), added rounded
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    sum[i][h] += acc[i][h];
+                    acc[i][h] = 0.0f;
+                }
+        }
     }
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int h = 0; h < 4; ++h)
+            acc[i][h] += sum[i][h];
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
         red[warp][8 * i + 2 * q][g] = acc[i][0];
