@@ -433,8 +433,8 @@ __global__ void __launch_bounds__(kAdWarps * 32, NT >= 8 ? 1 : 2) k_ad_inner(AdI
 // included); a warp multiplies 16 rows with half of the ranks over a part of a
 // stage, all its fragments loaded before the first product (a few warps hide
 // little latency).  Meant to be bound by the read of x; it waits for its stages
-// instead: 2.2 TB/s at rank 32 (8192 rows of 4096), a third of the copy bandwidth,
-// and 1.2 TB/s at rank 64 (8192 rows of 2048), a fifth.  An adapter's matrix is
+// instead: 2.0 TB/s at rank 32 (8192 rows of 4096), a third of the copy bandwidth,
+// and 1.1 TB/s at rank 64 (8192 rows of 2048), a sixth.  An adapter's matrix is
 // read, from L2, once for each 32 rows that have it (64 rows would halve that but
 // leave one CTA an SM: 43 against 33 us for the same rows).
 constexpr int kAdBigWarps = 16;
